@@ -19,6 +19,9 @@
  *   - Both pure-Python pages' "Extending It" roadmaps (attention split across
  *     devices, each holding part of the key/value space): the per-shard
  *     forward fa_forward_offset and the partial-result merge fa_merge.
+ * The norm and rotation before the attention (fa_norm_rope), the paged cache's
+ * writer (fa_append_paged) and the attention of several new tokens over it
+ * (fa_extend_paged) have no page: their formulas stand at their declarations.
  *
  * Conventions shared by every entry point
  *   - Layout: Q, K, V, O, dO, dQ, dK, dV are contiguous row-major
@@ -43,8 +46,9 @@
  *     combination with no kernel).  FA_ERR_CUDA reports a failed launch.
  *   - Kernels never trap.  A kernel that waits too long on an internal
  *     barrier records FA_ERR_TIMEOUT in a device status word and returns; a
- *     paged decode that meets a block id outside its pool skips that block and
- *     records FA_ERR_INVALID; fa_get_device_status() reports either.
+ *     paged call that meets a block id outside its pool skips that block and
+ *     records FA_ERR_INVALID, as does a rotation at a position outside its table;
+ *     fa_get_device_status() reports either.
  */
 #ifndef TILED_EXACT_ATTENTION_FA_H_
 #define TILED_EXACT_ATTENTION_FA_H_
@@ -259,9 +263,156 @@ FA_API fa_status fa_backward(const void* q, const void* k, const void* v, const 
                       fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Per-head RMS norm and position rotation of queries and keys, one pass:
+ *     r = 1 / sqrt(mean(x^2) + eps),  y = x r w,  z = R(p) y
+ * for every row x of d elements, R(p) turning pairs of the first `rot` elements by
+ * the angles of position p: (a, b) -> (a cos - b sin, b cos + a sin).  float32
+ * arithmetic, one rounding to the output's type.
+ *
+ *   q, k       : [B][Hq][N][d] and [B][Hk][N][d] (dtype FA_BF16, FA_FP16 or
+ *                FA_FP32; d = 64 or 128) at free strides, each row contiguous.
+ *                k may be NULL (Hk is then ignored).
+ *   q_out,
+ *   k_out      : outputs of the same sizes at strides of their own; an output
+ *                may be its input (same pointer and strides).
+ *   strides    : HOST array of 12: (batch, head, row) strides in elements of q, k,
+ *                q_out, k_out (k's unread without k).  Each is >= 0 and a
+ *                multiple of 16 bytes, and > 0 for the outputs, wherever the
+ *                dimension is above 1.  (A packed batch [T][H][d] is B = 1,
+ *                N = T, strides (0, d, H * d).)
+ *   q_weight,
+ *   k_weight   : [d] in `weight_dtype` (dtype or FA_FP32), or NULL for ones.
+ *   rope       : float32 [max_pos][rot]: row p holds rot/2 cosines, then rot/2
+ *                sines of position p's angles; 16-byte aligned.  NULL with
+ *                rot = 0: no rotation.
+ *   rot        : a multiple of 16 up to d; elements from rot on are not turned.
+ *   interleaved: 0: pair i is elements (i, i + rot/2); 1: (2i, 2i + 1).
+ *   positions  : int32 DEVICE array, row n of batch b at position
+ *                positions[b * pos_stride + n]; NULL: at position n.  A position
+ *                outside [0, max_pos) is never looked up: the row's rotated
+ *                elements come out NaN and FA_ERR_INVALID is recorded for
+ *                fa_get_device_status.
+ *   eps        : >= 0; a negative eps leaves the norm (and the weights) out.
+ * At least one of norm and rotation is wanted (FA_ERR_INVALID otherwise).
+ */
+FA_API fa_status fa_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const int64_t* strides,
+                              const void* q_weight, const void* k_weight, const float* rope,
+                              const int32_t* positions, long long pos_stride, int B, int Hq, int Hk, int N,
+                              int d, int rot, int max_pos, float eps, int interleaved, fa_dtype dtype,
+                              fa_dtype weight_dtype, void* stream);
+
+/* Bytes of device workspace fa_norm_rope_backward needs for weight gradients (a
+ * multiple of 256; 0 for a d without a kernel). */
+FA_API size_t fa_norm_rope_backward_workspace_size(int d);
+
+/*
+ * Backward of fa_norm_rope: with dz the gradient of an output row,
+ *     g = R(p)^T dz,  dw = sum over all rows of g x r,  u = g w,
+ *     dx = r (u - x r^2 mean(u x)).
+ *
+ *   q, k       : the forward's inputs (unread, and may be NULL, with eps < 0).
+ *   dq_out,
+ *   dk_out     : gradients of q_out and k_out; dk_out may be NULL: no k.
+ *   dq, dk     : gradients of q and k.
+ *   strides    : HOST array of 18: q, k, dq_out, dk_out, dq, dk, as above.
+ *   dq_weight,
+ *   dk_weight  : [d] outputs in `weight_dtype`, or NULL.  Summed in float32 in an
+ *                order that the sizes alone fix: equal calls give equal bits.
+ *   workspace  : >= fa_norm_rope_backward_workspace_size(d) bytes, 256-byte
+ *                aligned, contents ignored on entry; NULL without weight gradients.
+ * The other arguments are the forward's.
+ */
+FA_API fa_status fa_norm_rope_backward(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                                       void* dq, void* dk, const int64_t* strides, const void* q_weight,
+                                       const void* k_weight, void* dq_weight, void* dk_weight,
+                                       const float* rope, const int32_t* positions, long long pos_stride,
+                                       int B, int Hq, int Hk, int N, int d, int rot, int max_pos, float eps,
+                                       int interleaved, fa_dtype dtype, fa_dtype weight_dtype,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Append: the keys and values of packed new tokens into a paged cache, the keys
+ * (and, with q, the queries) normalised and rotated on the way as fa_norm_rope
+ * does it.
+ *
+ *   k, v        : [T][Hkv][d] (dtype FA_BF16 or FA_FP16, d = 128), heads contiguous,
+ *                 tokens k_stride and v_stride elements apart (multiples of 16
+ *                 bytes, >= Hkv * d), 16-byte aligned.
+ *   kpool, vpool,
+ *   block_table : as fa_decode_paged, with Hkv heads.  Written in place.
+ *   cu_tokens   : int32 DEVICE array [B + 1], non-decreasing: sequence b's new
+ *                 tokens are [cu_tokens[b], cu_tokens[b + 1]).  NULL: one token for
+ *                 each sequence (T = B).  Tokens outside every sequence are not
+ *                 read into anything: their outputs stay as they were.
+ *   seqlens     : int32 DEVICE array [B]: the lengths WITH the new tokens, so that
+ *                 the same array serves fa_extend_paged and fa_decode_paged next.
+ *                 Token t of sequence b takes position
+ *                 seqlens[b] - cu_tokens[b + 1] + t.
+ *   q, q_out    : [T][Hq][d], q at q_stride, q_out contiguous (q_out may be q where
+ *                 that is contiguous); both NULL: no queries.
+ *   q_weight, k_weight, rope, rot, max_pos, eps, interleaved, weight_dtype: as
+ *                 fa_norm_rope (without norm and rotation the keys are copied).
+ * A token whose position lies outside [0, max_blocks * block_size) or the table,
+ * or whose block id lies outside [0, num_blocks), is not written (its q_out row
+ * comes out NaN where it would be turned) and FA_ERR_INVALID is recorded for
+ * fa_get_device_status.
+ */
+FA_API fa_status fa_append_paged(const void* k, const void* v, const void* q, void* q_out, void* kpool,
+                                 void* vpool, const int32_t* block_table, const int32_t* cu_tokens,
+                                 const int32_t* seqlens, long long q_stride, long long k_stride,
+                                 long long v_stride, const void* q_weight, const void* k_weight,
+                                 const float* rope, int T, int B, int Hq, int Hkv, int num_blocks,
+                                 int block_size, int max_blocks, int d, int rot, int max_pos, float eps,
+                                 int interleaved, fa_dtype dtype, fa_dtype weight_dtype, void* stream);
+
+/* Bytes of device workspace fa_extend_paged needs for these sizes (a multiple of
+ * 256; 0 for invalid sizes). */
+FA_API size_t fa_extend_paged_workspace_size(int T, int Hq, int Hkv, int d);
+
+/*
+ * Chunk attention: packed new tokens attend to their sequences' paged caches, which
+ * hold them already (fa_append_paged).  Hq = G * Hkv query heads, query head h
+ * reading key head h / G.  With one token a sequence this is fa_decode_paged's
+ * attention with grouped heads.
+ *
+ *   q           : [T][Hq][d] (dtype FA_BF16 or FA_FP16, d = 128), heads contiguous,
+ *                 tokens q_stride elements apart (a multiple of 16 bytes,
+ *                 >= Hq * d), 16-byte aligned.
+ *   kpool, vpool,
+ *   block_table : as fa_decode_paged, with Hkv heads; Hq a multiple of Hkv, at
+ *                 most 128 times.
+ *   cu_tokens   : int32 DEVICE array [B + 1], non-decreasing, or NULL: one token for
+ *                 each sequence (T = B).  Values are clamped to [0, T].
+ *   seqlens     : int32 DEVICE array [B], the lengths with the new tokens, clamped
+ *                 to [0, max_blocks * block_size].
+ *   causal,
+ *   window      : token i of the m new ones of a sequence of length n sits at
+ *                 position p = n - m + i and sees key j < n iff (causal == 0 ||
+ *                 j <= p) && (window <= 0 || j > p - window).  Blocks that hold
+ *                 no key visible to any token of the sequence are never read, nor
+ *                 are their table entries.  window <= 2^29.
+ *   o           : [T][Hq][d] contiguous.  lse: [T][Hq] float32 or NULL.  A row that
+ *                 sees no key gets o = 0, lse = -inf; rows of tokens outside every
+ *                 sequence stay as they were.
+ *   workspace   : >= fa_extend_paged_workspace_size(T, Hq, Hkv, d) bytes, 256-byte
+ *                 aligned, contents ignored on entry.  Calls that may run at the
+ *                 same time need workspaces of their own.
+ * A block id outside [0, num_blocks) is skipped and recorded as in fa_decode_paged.
+ * A non-finite value row that a token sees makes its own output non-finite; it may
+ * do so, as 0 * inf, to the outputs of the tokens of the same chunk that precede it.
+ */
+FA_API fa_status fa_extend_paged(const void* q, const void* kpool, const void* vpool,
+                                 const int32_t* block_table, const int32_t* cu_tokens,
+                                 const int32_t* seqlens, void* o, float* lse, long long q_stride, int T,
+                                 int B, int Hq, int Hkv, int num_blocks, int block_size, int max_blocks,
+                                 int d, float scale, int causal, int window, fa_dtype dtype,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then returns FA_ERR_TIMEOUT if any kernel of this
  * library recorded a barrier timeout since the last call, FA_ERR_INVALID if
- * a paged decode met a block id outside its pool (either record is cleared),
+ * a paged call met a block id outside its pool or a position outside its table
+ * (either record is cleared),
  * FA_ERR_CUDA if the stream reports an error, else FA_OK.
  */
 FA_API fa_status fa_get_device_status(void* stream);

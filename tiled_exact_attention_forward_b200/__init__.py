@@ -14,6 +14,11 @@ Functions (names follow the C ABI):
              scale=None)                                         -> (dq, dk, dv)
     forward_offset(q, k, v, q_offset, causal=False, window=0)   -> (o, lse)
     merge(o_parts, lse_parts)                                    -> (o, lse)
+    norm_rope(q, k, q_weight, k_weight, rope, positions)         -> (q, k) normed and rotated
+    norm_rope_backward(q, k, dq_out, dk_out, ...)                -> (dq, dk, dq_weight, dk_weight)
+    qk_norm_rope(q, k, q_weight, k_weight, rope, positions)      -> the same (q, k), differentiable
+    append_paged(k, v, kpool, vpool, block_table, seqlens)       -> new tokens into a paged cache
+    extend_paged(q, kpool, vpool, block_table, seqlens)          -> (o, lse) of new tokens over it
     forward_host(...)  -- forward on pinned host tensors (copies in and out)
     forward_backward_host(...)  -- forward and backward on pinned host tensors
     attention(q, k, v, causal=False, window=0, scale=None)      -> o, differentiable
@@ -45,6 +50,12 @@ EXPORTED_SYMBOLS = (
     "fa_decode_paged",
     "fa_backward_workspace_size",
     "fa_backward",
+    "fa_norm_rope",
+    "fa_norm_rope_backward_workspace_size",
+    "fa_norm_rope_backward",
+    "fa_append_paged",
+    "fa_extend_paged_workspace_size",
+    "fa_extend_paged",
     "fa_get_device_status",
     "fa_selftest_wait_timeout",
     "fa_selftest_exp2_poly",
@@ -93,6 +104,19 @@ def _lib() -> ctypes.CDLL:
     lib.fa_backward_workspace_size.restype = Z
     lib.fa_backward.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, F, I, I, I, P, Z, P]
     lib.fa_backward.restype = I
+    L = ctypes.c_longlong
+    lib.fa_norm_rope.argtypes = [P] * 9 + [L] + [I] * 7 + [F, I, I, I, P]
+    lib.fa_norm_rope.restype = I
+    lib.fa_norm_rope_backward_workspace_size.argtypes = [I]
+    lib.fa_norm_rope_backward_workspace_size.restype = Z
+    lib.fa_norm_rope_backward.argtypes = [P] * 13 + [L] + [I] * 7 + [F, I, I, I, P, Z, P]
+    lib.fa_norm_rope_backward.restype = I
+    lib.fa_append_paged.argtypes = [P] * 9 + [L] * 3 + [P] * 3 + [I] * 10 + [F, I, I, I, P]
+    lib.fa_append_paged.restype = I
+    lib.fa_extend_paged_workspace_size.argtypes = [I, I, I, I]
+    lib.fa_extend_paged_workspace_size.restype = Z
+    lib.fa_extend_paged.argtypes = [P] * 8 + [L] + [I] * 8 + [F, I, I, I, P, Z, P]
+    lib.fa_extend_paged.restype = I
     lib.fa_selftest_wait_timeout.argtypes = [ctypes.c_longlong, P]
     lib.fa_selftest_wait_timeout.restype = I
     lib.fa_selftest_exp2_poly.argtypes = [P, P, ctypes.c_longlong, P]
@@ -443,6 +467,347 @@ def attention(q, k, v, causal: bool = False, window: int = 0, scale=None):
     d = 128 for the backward).  Gradients stay on the device.
     """
     return _Attention.apply(q, k, v, bool(causal), int(window), scale)
+
+
+class _On:
+    """Makes a tensor's device the current one for a launch (nothing to do when it is)."""
+
+    def __init__(self, device):
+        self.to = device.index
+
+    def __enter__(self):
+        self.was = torch.cuda.current_device()
+        if self.was != self.to:
+            torch.cuda.set_device(self.to)
+
+    def __exit__(self, *exc):
+        if self.was != self.to:
+            torch.cuda.set_device(self.was)
+
+
+def _need_on(device, **tensors):
+    """Each given tensor sits on `device`, a CUDA one (None entries are skipped)."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device (there is no CPU path)")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, as the first tensor is")
+
+
+def _need_int32(name, t, shape):
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+
+
+def _heads_view(t, what):
+    """Sizes (B, H, N, d) and (batch, head, row) strides of a [B, H, N, d] or packed [T, H, d] tensor."""
+    if t.dim() == 4:
+        B, H, N, d = t.shape
+        st = t.stride()
+        strides = st[:3]
+    elif t.dim() == 3:
+        N, H, d = t.shape
+        st = t.stride()
+        B, strides = 1, (0, st[1], st[0])
+    else:
+        raise ValueError(f"{what} must be [B, H, N, d] or packed [T, H, d]")
+    if st[-1] != 1:
+        raise ValueError(f"{what}: the rows (last dimension) must be contiguous")
+    return (B, H, N, d), strides
+
+
+def _grad_like(t):
+    """An uninitialised gradient laid out as t where t is dense, contiguous where not (expanded views)."""
+    g = torch.empty_like(t)
+    return g if g.stride(-1) == 1 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _rotation_args(q, q_weight, k_weight, rope, eps, d):
+    """(rot, max_pos, eps for the C ABI, weight dtype code) of a norm and rotation."""
+    rot = max_pos = 0
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous float32 tensor [positions, rot]: rot/2 cosines, rot/2 sines")
+        max_pos, rot = rope.shape
+        if rot == 0 or rot % 16 or rot > d:
+            raise ValueError("rope's second dimension must be a multiple of 16 up to the head dimension")
+    wdt = None
+    for w in (q_weight, k_weight):
+        if w is None:
+            continue
+        if eps is None:
+            raise ValueError("weights need eps: without it there is no norm")
+        if w.shape != (d,) or not w.is_contiguous():
+            raise ValueError("weights must be contiguous tensors of the head dimension")
+        if w.dtype not in (q.dtype, torch.float32) or (wdt is not None and w.dtype != wdt):
+            raise ValueError("weights must share one dtype: the tensors' or float32")
+        wdt = w.dtype
+    if eps is not None and not eps >= 0:
+        raise ValueError("eps must be >= 0 (None: no norm)")
+    return rot, max_pos, -1.0 if eps is None else float(eps), _dtype_code(wdt if wdt is not None else q.dtype)
+
+
+def _positions_args(positions, B, N):
+    if positions is None:
+        return 0
+    if positions.dtype != torch.int32 or positions.shape not in ((N,), (B, N)) or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int32 tensor [N] or [B, N] (packed: [T])")
+    return N if positions.dim() == 2 else 0
+
+
+def norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6,
+              interleaved: bool = False, q_out=None, k_out=None):
+    """Per-head RMS norm and position rotation of queries and keys in one launch.
+
+    q, k: [B, H, N, d] (or packed [T, H, d]) CUDA tensors, d in {64, 128}, bf16,
+    fp16 or float32, rows contiguous, other strides free (multiples of 16 bytes):
+    a transposed view of a projection's [B, N, H, d] output is read where it lies.
+    H may differ between q and k; k may be None.
+    y = x / sqrt(mean(x^2) + eps) * weight per row (weight [d], None for ones;
+    eps=None leaves the norm out), then the first rot elements turned by the angles of
+    the row's position.  rope: float32 [positions, rot], rot/2 cosines then rot/2
+    sines per position, rot a multiple of 16 (None: no rotation); pairs are
+    (i, i + rot/2), or (2i, 2i + 1) with interleaved.  positions: int32 [N] or [B, N]
+    (packed: [T]); None: 0 .. N-1.  A position outside the table gives NaN and is
+    reported by device_status().
+    Returns (q_out, k_out), contiguous [B, H, N, d] (or [T, H, d]), as the attention
+    calls take them; without k, q_out alone.  q_out, k_out may be given (at any
+    strides, the inputs themselves among them).
+    """
+    (B, Hq, N, d), qs = _heads_view(q, "q")
+    _need_on(q.device, k=k, q_weight=q_weight, k_weight=k_weight, rope=rope, positions=positions, q_out=q_out, k_out=k_out)
+    Hk, ks, kos = 0, (0, 0, 0), (0, 0, 0)
+    if k is not None:
+        kshape, ks = _heads_view(k, "k")
+        Hk = kshape[1]
+        if kshape != (B, Hk, N, d) or k.dim() != q.dim() or k.dtype != q.dtype:
+            raise ValueError("q and k must share dtype and every size but the heads")
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    rot, max_pos, e, wcode = _rotation_args(q, q_weight, k_weight, rope, eps, d)
+    pos_stride = _positions_args(positions, B, N)
+    for x, out in ((q, q_out), (k, k_out)):
+        if out is not None and (out.shape != x.shape or out.dtype != x.dtype):
+            raise ValueError("an output must have its input's shape and dtype")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    qos = _heads_view(q_out, "q_out")[1]
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        kos = _heads_view(k_out, "k_out")[1]
+    with _On(q.device):
+        st = _lib().fa_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out),
+                                 (ctypes.c_longlong * 12)(*qs, *ks, *qos, *kos), _ptr(q_weight), _ptr(k_weight),
+                                 _ptr(rope), _ptr(positions), pos_stride, B, Hq, Hk, N, d, rot, max_pos, e,
+                                 int(bool(interleaved)), _dtype_code(q.dtype), wcode, _stream(q.device))
+    _check(st, "fa_norm_rope")
+    return (q_out, k_out) if k is not None else q_out
+
+
+def norm_rope_backward_workspace_size(d) -> int:
+    return int(_lib().fa_norm_rope_backward_workspace_size(d))
+
+
+def norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6,
+                       interleaved: bool = False, workspace=None):
+    """Gradients of norm_rope: (dq, dk, dq_weight, dk_weight).
+
+    q, k: the forward's inputs; dq_out, dk_out: the gradients of its outputs, of the
+    same sizes, rows contiguous.  k and dk_out may be None together (dk is then
+    None).  dq and dk are laid out as q and k are (dense in their strides' order).
+    A weight that is None has no gradient (None); weight gradients are summed in
+    float32 in a fixed order and come in the weights' dtype.
+    """
+    (B, Hq, N, d), qs = _heads_view(q, "q")
+    _need_on(q.device, k=k, dq_out=dq_out, dk_out=dk_out, q_weight=q_weight, k_weight=k_weight, rope=rope,
+             positions=positions, workspace=workspace)
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out go together")
+    Hk, ks, kgs, dks = 0, (0, 0, 0), (0, 0, 0), (0, 0, 0)
+    if dq_out.shape != q.shape or dq_out.dtype != q.dtype:
+        raise ValueError("dq_out must have q's shape and dtype")
+    qgs = _heads_view(dq_out, "dq_out")[1]
+    dq, dk = _grad_like(q), None
+    if k is not None:
+        kshape, ks = _heads_view(k, "k")
+        Hk = kshape[1]
+        if kshape != (B, Hk, N, d) or k.dim() != q.dim() or k.dtype != q.dtype:
+            raise ValueError("q and k must share dtype and every size but the heads")
+        if dk_out.shape != k.shape or dk_out.dtype != k.dtype:
+            raise ValueError("dk_out must have k's shape and dtype")
+        kgs = _heads_view(dk_out, "dk_out")[1]
+        dk = _grad_like(k)
+        dks = _heads_view(dk, "dk")[1]
+    elif k_weight is not None:
+        raise ValueError("k_weight needs k")
+    rot, max_pos, e, wcode = _rotation_args(q, q_weight, k_weight, rope, eps, d)
+    pos_stride = _positions_args(positions, B, N)
+    dqw = None if q_weight is None else torch.empty_like(q_weight)
+    dkw = None if k_weight is None else torch.empty_like(k_weight)
+    ws_bytes = 0
+    if dqw is not None or dkw is not None:
+        if workspace is None:
+            workspace = torch.empty(norm_rope_backward_workspace_size(d), dtype=torch.uint8, device=q.device)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    with _On(q.device):
+        st = _lib().fa_norm_rope_backward(
+            _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk),
+            (ctypes.c_longlong * 18)(*qs, *ks, *qgs, *kgs, *_heads_view(dq, "dq")[1], *dks), _ptr(q_weight),
+            _ptr(k_weight), _ptr(dqw), _ptr(dkw), _ptr(rope), _ptr(positions), pos_stride, B, Hq, Hk, N, d, rot, max_pos,
+            e, int(bool(interleaved)), _dtype_code(q.dtype), wcode, _ptr(workspace), ws_bytes, _stream(q.device))
+    _check(st, "fa_norm_rope_backward")
+    return dq, dk, dqw, dkw
+
+
+class _QKNormRope(torch.autograd.Function):
+    """Saves the inputs; the backward recomputes the rows' norms from them."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, rope, positions, eps, interleaved):
+        ctx.save_for_backward(q, k, q_weight, k_weight, rope, positions)
+        ctx.how = (eps, interleaved)
+        return norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved)
+
+    @staticmethod
+    def backward(ctx, gq, gk=None):
+        q, k, q_weight, k_weight, rope, positions = ctx.saved_tensors
+        gq = gq if gq.stride(-1) == 1 else gq.contiguous()
+        if gk is not None and gk.stride(-1) != 1:
+            gk = gk.contiguous()
+        dq, dk, dqw, dkw = norm_rope_backward(q, k, gq, gk, q_weight, k_weight, rope, positions, *ctx.how)
+        return dq, dk, dqw, dkw, None, None, None, None
+
+
+def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6,
+                 interleaved: bool = False):
+    """norm_rope with autograd: gradients for q, k and the weights (rope and positions have none).
+
+    The step before ``attention``: q, k = qk_norm_rope(q, k, ...); o = attention(q, k, v, causal=True).
+    To capture forward and backward into a CUDA graph, drop every eager autograd graph of the
+    same leaves first, as torch's graph capture asks of any differentiable operation.
+    """
+    return _QKNormRope.apply(q, k, q_weight, k_weight, rope, positions, eps, bool(interleaved))
+
+
+def _packed(name, t, H, d, dtype):
+    """The token stride of a packed [T, H, d] tensor whose heads are contiguous."""
+    if t.dim() != 3 or t.shape[1:] != (H, d) or t.dtype != dtype:
+        raise ValueError(f"{name} must be [T, {H}, {d}] with the pools' dtype")
+    st = t.stride()
+    if st[2] != 1 or (H > 1 and st[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st[0]
+
+
+def _paged_args(kpool, vpool, block_table, seqlens, cu_tokens, T):
+    """(num_blocks, Hkv, block_size, d, B, max_blocks) of a paged cache, its tensors checked."""
+    if kpool.dim() != 4 or vpool.shape != kpool.shape or vpool.dtype != kpool.dtype:
+        raise ValueError("kpool and vpool must be [num_blocks, Hkv, block_size, d] and share dtype")
+    if not (kpool.is_contiguous() and vpool.is_contiguous()):
+        raise ValueError("kpool and vpool must be contiguous")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 tensor of shape [B, max_blocks]")
+    B, max_blocks = block_table.shape
+    _need_int32("block_table", block_table, (B, max_blocks))
+    _need_int32("seqlens", seqlens, (B,))
+    if cu_tokens is not None:
+        _need_int32("cu_tokens", cu_tokens, (B + 1,))
+    elif T != B:
+        raise ValueError("without cu_tokens there is one token for each sequence")
+    return (*kpool.shape, B, max_blocks)
+
+
+def append_paged(k, v, kpool, vpool, block_table, seqlens, cu_tokens=None, rope=None, q=None, q_weight=None,
+                 k_weight=None, eps=None, interleaved: bool = False, q_out=None):
+    """New tokens' keys and values into a paged cache, in place, the keys rotated on the way.
+
+    k, v: packed [T, Hkv, d] CUDA tensors (bf16 or fp16, d = 128), tokens at any stride
+    (views of a fused projection).  kpool, vpool, block_table as decode_paged takes
+    them.  cu_tokens: int32 [B + 1], sequence b's tokens are cu_tokens[b] ..
+    cu_tokens[b + 1] - 1 (None: one token each, T = B).  seqlens: int32 [B], the
+    lengths WITH the new tokens: the tokens take the last positions, and the same
+    array serves extend_paged and decode_paged.
+    Keys are normed (eps given, weight k_weight or ones) and turned by rope as in
+    norm_rope; values are copied.  q, packed [T, Hq, d], is normed with q_weight and
+    turned in the same launch: returned contiguous (None without q).
+    A token without a place (position outside the cache or the table, block id outside
+    the pool) is not written and reported by device_status().
+    """
+    _need_on(k.device, v=v, q=q, q_out=q_out, kpool=kpool, vpool=vpool, block_table=block_table, seqlens=seqlens,
+             cu_tokens=cu_tokens, rope=rope, q_weight=q_weight, k_weight=k_weight)
+    T = k.shape[0]
+    num_blocks, Hkv, bs, d, B, max_blocks = _paged_args(kpool, vpool, block_table, seqlens, cu_tokens, T)
+    k_stride, v_stride = _packed("k", k, Hkv, d, kpool.dtype), _packed("v", v, Hkv, d, kpool.dtype)
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same tokens")
+    rot, max_pos, e, wcode = _rotation_args(k, q_weight, k_weight, rope, eps, d)
+    Hq = q_stride = 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        q_stride = _packed("q", q, Hq, d, kpool.dtype)
+        if q.shape[0] != T:
+            raise ValueError("q and k must have the same tokens")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous with q's shape and dtype")
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    with _On(k.device):
+        st = _lib().fa_append_paged(_ptr(k), _ptr(v), _ptr(q), _ptr(q_out), _ptr(kpool), _ptr(vpool), _ptr(block_table),
+                                    _ptr(cu_tokens), _ptr(seqlens), q_stride, k_stride, v_stride, _ptr(q_weight),
+                                    _ptr(k_weight), _ptr(rope), T, B, Hq, Hkv, num_blocks, bs, max_blocks, d, rot,
+                                    max_pos, e, int(bool(interleaved)), _dtype_code(kpool.dtype), wcode,
+                                    _stream(k.device))
+    _check(st, "fa_append_paged")
+    return q_out
+
+
+def extend_paged_workspace_size(T, Hq, Hkv, d) -> int:
+    return int(_lib().fa_extend_paged_workspace_size(T, Hq, Hkv, d))
+
+
+def extend_paged(q, kpool, vpool, block_table, seqlens, cu_tokens=None, causal: bool = True, window: int = 0, scale=None,
+                 workspace=None, out=None, lse=None):
+    """Attention of packed new tokens over a paged cache that holds them already.
+
+    q: packed [T, Hq, d] CUDA tensor (bf16 or fp16, d = 128), tokens at any stride;
+    pools, block_table, seqlens and cu_tokens as append_paged takes them, Hq a
+    multiple of the pools' heads (query head h reads key head h * Hkv // Hq).  Token i
+    of the m new ones of a sequence of length n sits at position n - m + i and sees
+    the keys up to itself (causal), the last `window` of them with window > 0.
+    Returns (o [T, Hq, d], lse [T, Hq] float32); o = 0 and lse = -inf for a token that
+    sees no key; tokens outside every sequence keep what out and lse held.  Calls that
+    may overlap need workspaces of their own (the default makes one).  An out-of-range
+    block id of a used block is skipped and reported by device_status().
+    """
+    _need_on(q.device, kpool=kpool, vpool=vpool, block_table=block_table, seqlens=seqlens, cu_tokens=cu_tokens,
+             workspace=workspace, out=out, lse=lse)
+    if q.dim() != 3:
+        raise ValueError("q must be packed [T, Hq, d]")
+    T, Hq = q.shape[:2]
+    num_blocks, Hkv, bs, d, B, max_blocks = _paged_args(kpool, vpool, block_table, seqlens, cu_tokens, T)
+    q_stride = _packed("q", q, Hq, d, kpool.dtype)
+    if Hkv < 1 or Hq % Hkv:
+        raise ValueError("the query heads must be a multiple of the pools' heads")
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous with q's shape and dtype")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    elif lse.shape != (T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 tensor [T, Hq]")
+    if workspace is None:
+        workspace = torch.empty(max(extend_paged_workspace_size(T, Hq, Hkv, d), 256), dtype=torch.uint8, device=q.device)
+    with _On(q.device):
+        st = _lib().fa_extend_paged(_ptr(q), _ptr(kpool), _ptr(vpool), _ptr(block_table), _ptr(cu_tokens), _ptr(seqlens),
+                                    _ptr(out), _ptr(lse), q_stride, T, B, Hq, Hkv, num_blocks, bs, max_blocks, d,
+                                    _scale_arg(scale), int(bool(causal)), int(window), _dtype_code(q.dtype),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(q.device))
+    _check(st, "fa_extend_paged")
+    return out, lse
 
 
 def selftest_wait_timeout(limit_cycles: int = 20_000_000, device=None) -> int:

@@ -9,9 +9,10 @@ Each source is compiled to an object of its own (in parallel) as whole-program
 device code -- one module per source file, no device linking: under separate
 compilation (-rdc) ptxas ignores the per-warpgroup register budgets that the
 forward kernel sets with setmaxnreg -- then one nvcc call links them.  Flags can differ per file: the
-float32 forward (the exact path of the single-head fp32 workload) is built
-without ``--use_fast_math`` so its exp2, log and division are the IEEE-rounded
-ones; every other kernel calls its fast instructions explicitly and keeps the
+float32 forward (the exact path of the single-head fp32 workload) and the
+norm-and-rotate kernels (float32 in and out among their types) are built without
+``--use_fast_math`` so their exp2, log, square root and division are the
+IEEE-rounded ones; every other kernel calls its fast instructions explicitly and keeps the
 fast-math flags it was measured with.
 """
 from __future__ import annotations
@@ -38,7 +39,7 @@ COMMON_FLAGS = [
 ]
 FAST_MATH = ["--use_fast_math"]
 # Sources built with IEEE-rounded float32 math (no --use_fast_math).
-EXACT_MATH_SOURCES = {"fwd_f32.cu"}
+EXACT_MATH_SOURCES = {"fwd_f32.cu", "norm_rope.cu", "append_paged.cu"}
 
 
 def nvcc() -> str:

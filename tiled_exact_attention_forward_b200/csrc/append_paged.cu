@@ -1,0 +1,152 @@
+// New tokens' keys and values into a paged cache, the keys (and, asked for, the
+// queries) normalised and rotated on the way.
+//
+// Token t of the packed batch belongs to the sequence b with cu_tokens[b] <= t <
+// cu_tokens[b + 1] and takes position p = seqlens[b] - cu_tokens[b + 1] + t, so the
+// lengths count the new tokens already, as the decode and chunk attention calls
+// want them.  Its keys go to row p % block_size of block block_table[b][p / block_size].
+// The arithmetic per row is the norm-and-rotate kernel's (norm_rope.cu).
+//
+// Bound by memory for many tokens (each row read once and written once), by the
+// chain cu_tokens -> seqlens -> block_table -> store for few: the rows' loads are
+// issued ahead of that chain, and 16 lanes search cu_tokens together.
+#include "common.cuh"
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace fa {
+namespace app {
+
+using namespace rows;
+
+constexpr int D = 128;
+constexpr int L = D / 8;
+constexpr int THREADS = 256;
+constexpr int TOKENS = THREADS / L;  // tokens per block
+constexpr int HG = 4;                // heads per group of lanes
+
+// Number of i in [0, B) with cu[i + 1] <= t, for a non-decreasing cu: the lanes of the
+// row probe 16 places at once.  Every answer lies in [0, B], whatever cu holds.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int B, long long t, int s) {
+  const unsigned mask = 0xffffu << (threadIdx.x & 16);
+  int lo = 0, hi = B;
+  while (lo < hi) {
+    const int step = (hi - lo + L - 1) / L;
+    const int i = lo + (s + 1) * step - 1;  // last place of this lane's run
+    const bool below = i < hi && cu[i + 1] <= t;
+    const int runs = __popc(__ballot_sync(mask, below));
+    lo = min(hi, lo + runs * step);
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
+template <class E, bool INTER, bool NORM>
+__global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ AppendArgs a) {
+  const int s = threadIdx.x % L;
+  const int gq = a.q ? (a.Hq + HG - 1) / HG : 0, gk = (a.Hkv + HG - 1) / HG;
+  const int hg = blockIdx.x % (gq + 2 * gk);
+  const long long t = static_cast<long long>(blockIdx.x / (gq + 2 * gk)) * TOKENS + threadIdx.x / L;
+  const bool live = t < a.T;
+  const int kind = hg < gq ? 0 : hg < gq + gk ? 1 : 2;  // queries, keys, values
+  const int h0 = (kind == 0 ? hg : kind == 1 ? hg - gq : hg - gq - gk) * HG;
+  const int heads = min(HG, (kind == 0 ? a.Hq : a.Hkv) - h0);
+  const void* src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+  const long long stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+  const Lane l = lane_of<D, INTER>(s, a.rot);
+
+  uint2 rlo[HG], rhi[HG];
+  const long long x0 = t * stride + static_cast<long long>(h0) * D;
+#pragma unroll
+  for (int h = 0; h < HG; ++h) {
+    rlo[h] = rhi[h] = make_uint2(0u, 0u);
+    if (live && h < heads) {
+      rlo[h] = load4<E>(src, x0 + h * D + l.lo);
+      rhi[h] = load4<E>(src, x0 + h * D + l.hi);
+    }
+  }
+  float wlo[4], whi[4];
+  if (NORM && kind < 2) load_weight<E>(kind == 0 ? a.q_weight : a.k_weight, a.w_f32, l, wlo, whi);
+
+  // The token's place.  A token past the last sequence has none and writes nothing.
+  int b = 0;
+  bool placed = false;
+  long long pos = -1;
+  if (live) {
+    if (a.cu_tokens == nullptr) {
+      b = static_cast<int>(t);
+      placed = true;
+      pos = static_cast<long long>(a.seqlens[b]) - 1;
+    } else {
+      b = sequence_of(a.cu_tokens, a.B, t, s);
+      if (b < a.B && a.cu_tokens[b] <= t) {
+        placed = true;
+        pos = static_cast<long long>(a.seqlens[b]) - a.cu_tokens[b + 1] + t;
+      }
+    }
+  }
+  // Checked before anything is read or written through it: the position against the
+  // table's rows and the cache's capacity, the block id against the pool.
+  const long long cap = static_cast<long long>(a.max_blocks) << a.block_shift;
+  bool good = placed && pos >= 0 && pos < cap && (a.rot == 0 || pos < a.max_pos);
+  int phys = -1;
+  if (good && kind != 0) {
+    phys = a.block_table[static_cast<long long>(b) * a.max_blocks + (pos >> a.block_shift)];
+    good = phys >= 0 && phys < a.num_blocks;
+  }
+  if (placed && !good && s == 0) atomicOr(&g_status, kStatusBadBlock);
+
+  float c[4], sn[4];
+  load_angles(a.rope, pos, good, a.rot, s, l.turn && placed && kind < 2, c, sn);
+
+  void* dst = kind == 0 ? a.q_out : kind == 1 ? a.kpool : a.vpool;
+  const long long row0 = kind == 0 ? t * a.Hq + h0
+                                   : ((static_cast<long long>(phys) * a.Hkv + h0) << a.block_shift) +
+                                         (pos & ((1 << a.block_shift) - 1));
+  const long long next = kind == 0 ? 1 : 1LL << a.block_shift;
+#pragma unroll
+  for (int h = 0; h < HG; ++h) {
+    float lo[4], hi[4];
+    unpack4<E>(rlo[h], lo);
+    unpack4<E>(rhi[h], hi);
+    if (NORM && kind < 2) {
+      const float r = 1.f / sqrtf(row_sum<L>(dot8(lo, hi, lo, hi)) * (1.f / D) + a.eps);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] *= r * wlo[i];
+        hi[i] *= r * whi[i];
+      }
+    }
+    if (kind < 2) {
+      if (l.turn) rotate<INTER>(lo, hi, c, sn);
+      rlo[h] = pack4<E>(lo);
+      rhi[h] = pack4<E>(hi);
+    }
+    // A query without a place in the cache or the table comes out NaN where it is rotated.
+    if ((kind == 0 ? placed : good) && h < heads) {
+      store4<E>(dst, (row0 + h * next) * D + l.lo, rlo[h]);
+      store4<E>(dst, (row0 + h * next) * D + l.hi, rhi[h]);
+    }
+  }
+}
+
+template <class E>
+cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
+  const long long groups = (a.q ? (a.Hq + HG - 1) / HG : 0) + 2LL * ((a.Hkv + HG - 1) / HG);
+  const long long blocks = (static_cast<long long>(a.T) + TOKENS - 1) / TOKENS * groups;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  auto kernel = a.interleaved ? (a.norm ? append_kernel<E, true, true> : append_kernel<E, true, false>)
+                              : (a.norm ? append_kernel<E, false, true> : append_kernel<E, false, false>);
+  kernel<<<static_cast<unsigned>(blocks), THREADS, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace app
+
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
+  return a.f16 ? app::launch<F16>(a, stream) : app::launch<Bf16>(a, stream);
+}
+
+cudaError_t take_status_append(unsigned int* out) { return take_local_status(out); }
+
+}  // namespace fa

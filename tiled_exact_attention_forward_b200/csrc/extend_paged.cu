@@ -1,0 +1,1081 @@
+// Attention of packed new tokens over a paged cache (bf16 or f16, d = 128), causal at
+// the tokens' places in their sequences, with grouped heads: from one token a
+// sequence (decode) to long pieces of a prompt, mixed in one call.
+//
+//   o_r = sum_j softmax_j(q_r . k_j * scale) v_j over the keys j that row r sees,
+//   lse_r = ln sum_j exp(q_r . k_j * scale),
+// computed tile by tile with the online softmax, as in fwd_tc.cu.
+//
+// Rows.  The G = Hq / Hkv query heads of a key head read the same keys, so an item's
+// rows are (token, head of the group) pairs: a tile of 128 rows holds 128 / G tokens
+// of one sequence, and a K/V tile is loaded once for all of them.  An item is up to
+// two row tiles of one (sequence, key head):
+//   two tiles  -- both stream the same key tiles, one MMA/softmax ping-pong (as in
+//                 fwd_tc.cu);
+//   one tile   -- (single tokens, short or last pieces) the two softmax warpgroups
+//                 take the even and the odd key tiles of the same rows, so the
+//                 S -> softmax -> PV chain of one key tile overlaps the next one's;
+//                 the epilogue joins the two states.
+//
+// Work split.  One persistent CTA per SM.  An item costs one unit for itself and one
+// per key tile; all items laid end to end are cut into equal runs of units, one per
+// CTA, whatever the lengths: a long sequence with few rows is spread over many CTAs,
+// many short ones share a CTA.  An item cut by a run's edge leaves normalised float32
+// partials and their logsumexp in the workspace, and combine_kernel joins them (in
+// the order of the keys: the result does not depend on timing).  Every CTA works the
+// split out for itself from cu_tokens and seqlens, so no length crosses to the host.
+//
+// Cache.  K and V tiles come by TMA, one box per block and 64-column half; blocks
+// with no visible key are not read.  Rows of a V tile outside the item's keys (a
+// block's unused tail, a skipped block) are zeroed in shared memory before the MMA:
+// their weights are zero, but 0 * NaN is not.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace fa {
+namespace ext {
+
+constexpr int BM = 128;                     // rows per tile
+constexpr int BN = 128;                     // keys per tile
+constexpr int D = 128;
+constexpr int NS = 4;                       // K/V ring stages (K and V tiles interleaved)
+constexpr int TILE_BYTES = BM * D * 2;
+constexpr int HALF_BYTES = TILE_BYTES / 2;  // one 64-column half (128-byte rows, swizzled)
+constexpr int NUM_THREADS = 512;
+constexpr int WARPS = NUM_THREADS / 32;
+constexpr int WG_THREADS = 128;
+constexpr int EPI_WG = 2;
+constexpr int MMA_WARP = 12;
+constexpr int KV_WARP = 13;
+constexpr int Q_WARP = 14;
+constexpr int PLAN_WARP = 15;
+constexpr int NP = 4;                       // pieces in flight between the planner and the other warps
+constexpr int kPieceReaders = 15;           // warps that read a piece: MMA, K/V, Q, 8 softmax, 4 epilogue
+constexpr int kSoftmaxRegs = 192;
+constexpr int kEpilogueRegs = 64;
+constexpr int kOtherRegs = 64;
+constexpr int kLaunchRegs = 128;            // 65536 / NUM_THREADS: what the split draws on
+static_assert(2 * WG_THREADS * kSoftmaxRegs + WG_THREADS * kEpilogueRegs + WG_THREADS * kOtherRegs <=
+                  NUM_THREADS * kLaunchRegs,
+              "register split exceeds the launch budget");
+constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
+// A CTA takes at least this many units, so that few keys are not scattered over so
+// many CTAs that joining them costs more than it saves.
+constexpr int kMinUnits = 3;
+
+// A run of key tiles [j0, j1) of one item, as the planner hands it to the other warps.
+struct Piece {
+  int tok0, ntok;      // the item's tokens in the packed batch
+  int pos0;            // position of the first one in its sequence
+  int kvh, b;
+  int j0, j1;
+  int key_lo, key_hi;  // keys of the sequence that some row of the item sees
+  int slot;            // workspace slot of the partial result, -1: the piece is the whole item
+  int stop;            // no more pieces
+  int pad;
+};
+
+struct Smem {
+  uint8_t q[2][TILE_BYTES];
+  uint8_t kv[NS][TILE_BYTES];
+  uint8_t stage[4][HALF_BYTES / 4];  // epilogue, per warp: 32 rows of 128 bytes
+  uint32_t bad[4][BN / 32];          // keys of a tile whose block lies outside the pool
+  Piece piece[NP];
+  uint64_t piece_full[NP], piece_empty[NP];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[NS], kv_empty[NS];
+  uint64_t s_full[2];
+  uint64_t p_full[2];
+  uint64_t o_full[2], o_free[2];
+  uint64_t st_full[2], st_empty[2];
+  uint64_t mma_done;
+  float stat_m[2][BM], stat_l[2][BM];
+  long long scan[WARPS];
+  long long start_unit;              // units before the sequence the run starts in
+  long long start_units;             // its units per key head
+  int start_b;                       // that sequence
+  uint32_t tmem_base;
+  int abort_flag;
+};
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// Sizes and mask of a launch, in registers.
+struct Geo {
+  int T, B, Hq, Hkv, G, tpt;  // tpt: tokens per row tile, 128 / G
+  int causal, window, cap;
+};
+
+struct Seq {
+  int tok0, nq, n;  // first packed token, new tokens, keys
+};
+__device__ __forceinline__ Seq seq_of(const ExtendArgs& a, const Geo& g, int b) {
+  Seq s;
+  if (a.cu_tokens == nullptr) {
+    s.tok0 = b;
+    s.nq = 1;
+  } else {
+    s.tok0 = min(max(a.cu_tokens[b], 0), g.T);
+    s.nq = min(max(a.cu_tokens[b + 1], s.tok0), g.T) - s.tok0;
+  }
+  s.n = min(max(a.seqlens[b], 0), g.cap);
+  return s;
+}
+
+// Keys [lo, hi) that tokens at positions pf .. pl of a sequence with n keys see in all
+// (empty: lo = hi = 0).
+__device__ __forceinline__ void key_range(const Geo& g, int pf, int pl, int n, int& lo, int& hi) {
+  hi = g.causal ? min(n, pl + 1) : n;
+  lo = g.window > 0 ? max(0, pf - g.window + 1) : 0;
+  if (hi <= lo) lo = hi = 0;
+}
+// Key tiles of item p (tokens [2 tpt p, 2 tpt (p + 1)) of the sequence).
+__device__ __forceinline__ int item_tiles(const Geo& g, const Seq& s, int p, int& lo, int& hi) {
+  const int i0 = p * 2 * g.tpt, i1 = min(s.nq, i0 + 2 * g.tpt);
+  key_range(g, s.n - s.nq + i0, s.n - s.nq + i1 - 1, s.n, lo, hi);
+  return hi > lo ? (hi + BN - 1) / BN - lo / BN : 0;
+}
+__device__ __forceinline__ int items_of(const Geo& g, int nq) { return (nq + 2 * g.tpt - 1) / (2 * g.tpt); }
+
+// Units of all items of one key head of each lane's sequence (lane: its own `s`, nq = 0
+// for none).  Sequences with many items are summed by the whole warp.
+__device__ __forceinline__ long long head_units(const Geo& g, const Seq& s, int lane) {
+  const int np = items_of(g, s.nq);
+  long long u = 0;
+  int lo, hi;
+  if (np <= 4)
+    for (int p = 0; p < np; ++p) u += 1 + item_tiles(g, s, p, lo, hi);
+  unsigned many = __ballot_sync(0xffffffffu, np > 4);
+  while (many) {
+    const int src = __ffs(many) - 1;
+    many &= many - 1;
+    const Seq o{__shfl_sync(0xffffffffu, s.tok0, src), __shfl_sync(0xffffffffu, s.nq, src),
+                __shfl_sync(0xffffffffu, s.n, src)};
+    const int onp = items_of(g, o.nq);
+    long long v = 0;
+    for (int p = lane; p < onp; p += 32) v += 1 + item_tiles(g, o, p, lo, hi);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+    if (lane == src) u = v;
+  }
+  return u;
+}
+
+// The key tiles of piece p that slot t works on: first, end (exclusive) and step.
+struct Tiles {
+  int first, end, step;
+  __device__ __forceinline__ bool any() const { return first < end; }
+  __device__ __forceinline__ bool has(int j) const { return j >= first && j < end; }  // two-tile items only
+};
+__device__ __forceinline__ bool one_tile(const Geo& g, const Piece& p) { return p.ntok <= g.tpt; }
+__device__ __forceinline__ Tiles slot_tiles(const Geo& g, const Piece& p, int t) {
+  if (one_tile(g, p)) return Tiles{p.j0 + t, p.j1, 2};
+  const int i0 = t * g.tpt, i1 = min(p.ntok, i0 + g.tpt);
+  int lo = p.key_lo, hi = p.key_hi;
+  if (g.causal) hi = min(hi, p.pos0 + i1);
+  if (g.window > 0) lo = max(lo, p.pos0 + i0 - g.window + 1);
+  if (hi <= lo) return Tiles{p.j0, p.j0, 1};
+  return Tiles{max(p.j0, lo / BN), min(p.j1, (hi + BN - 1) / BN), 1};
+}
+// Rows of row tile t that hold a token.
+__device__ __forceinline__ int tile_rows(const Geo& g, const Piece& p, int t) {
+  return max(0, min(p.ntok - t * g.tpt, g.tpt)) * g.G;
+}
+
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+
+__device__ __forceinline__ void commit_elect(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+// S = Q K^T and O += P V for one tile; operand layouts as in fwd_tc.cu.
+template <class T>
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_addr, uint32_t k_addr) {
+  constexpr uint32_t h = HALF_BYTES >> 4, idesc = idesc_f32acc<T>(BM, BN, 0, 0);
+  mma8_ss<idesc, 2, 4, 6, h, h + 2, h + 4, h + 6>(d_tmem, desc_lo(q_addr, 16), desc_lo(k_addr, 16), desc_hi(1024), 0u);
+}
+template <class T>
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_addr, uint32_t accumulate) {
+  constexpr uint32_t idesc = idesc_f32acc<T>(BM, D, 0, 1), col_step = 8, v_step = (16 * 128) >> 4;
+  mma8_ts<idesc, col_step, v_step>(d_tmem, p_tmem, desc_lo(v_addr, HALF_BYTES), desc_hi(1024), accumulate);
+}
+
+#define FA_TMEM_LD16(taddr, r)                                                                       \
+  asm volatile(                                                                                      \
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"   \
+      "%15}, [%16];"                                                                                 \
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),          \
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),      \
+        "=r"(r[14]), "=r"(r[15])                                                                     \
+      : "r"(taddr))
+
+// A warp's view of the planner's ring of pieces.
+struct Pieces {
+  Smem* sm;
+  volatile int* abort_flag;
+  int i = 0;
+  // The next piece; false at the end (or when the CTA gives up).
+  __device__ __forceinline__ bool next(Piece& p, int lane) {
+    const int s = i % NP;
+    if (!mbar_wait_warp(smem_u32(&sm->piece_full[s]), (i / NP) & 1, abort_flag)) return false;
+    p = sm->piece[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm->piece_empty[s]));
+    ++i;
+    return !p.stop;
+  }
+};
+
+// Zeroes the rows of a V tile that hold no key of the item: rows outside [lo, hi) and
+// rows of blocks outside the pool.  All lanes; ends with the writes visible to the MMA.
+__device__ __forceinline__ void zero_v_rows(uint32_t v_addr, int lo, int hi, const uint32_t* bad, int lane) {
+  const uint32_t dst = v_addr + (lane >> 3 & 1) * HALF_BYTES + (lane & 7) * 16;
+#pragma unroll 1
+  for (int r = lane >> 4; r < BN; r += 2) {
+    if (r >= lo && r < hi && !((bad[r >> 5] >> (r & 31)) & 1u)) continue;
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + r * 128), "r"(0u) : "memory");
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+template <class T>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ExtendArgs args, int q_box_tokens) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int wg = warp >> 2;
+  Geo geo;
+  geo.T = args.T; geo.B = args.B; geo.Hq = args.Hq; geo.Hkv = args.Hkv;
+  geo.G = args.Hq / args.Hkv;
+  geo.tpt = BM / geo.G;
+  geo.causal = args.causal; geo.window = args.window; geo.cap = args.cap;
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&sm.q_full[t]), 1);
+      mbar_init(smem_u32(&sm.q_empty[t]), 1);
+      mbar_init(smem_u32(&sm.s_full[t]), 1);
+      mbar_init(smem_u32(&sm.p_full[t]), WG_THREADS);
+      mbar_init(smem_u32(&sm.o_full[t]), 1);
+      mbar_init(smem_u32(&sm.o_free[t]), WG_THREADS);
+      mbar_init(smem_u32(&sm.st_full[t]), WG_THREADS);
+      mbar_init(smem_u32(&sm.st_empty[t]), WG_THREADS);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_u32(&sm.kv_full[s]), 1);
+      mbar_init(smem_u32(&sm.kv_empty[s]), 1);
+    }
+    for (int s = 0; s < NP; ++s) {
+      mbar_init(smem_u32(&sm.piece_full[s]), 1);
+      mbar_init(smem_u32(&sm.piece_empty[s]), kPieceReaders);
+    }
+    mbar_init(smem_u32(&sm.mma_done), 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(smem_u32(&sm.tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (warp == KV_WARP && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+
+  // ------------------------------------------------------------ this CTA's run of units
+  // Total units, then the sequence in which the run starts.  Up to NUM_THREADS sequences
+  // are held one to a thread; more are walked in chunks, twice.
+  long long total = 0, mine = 0;
+  long long mine_units = 0;
+  for (int c = 0; c < geo.B; c += NUM_THREADS) {
+    Seq s{0, 0, 0};
+    if (c + static_cast<int>(threadIdx.x) < geo.B) s = seq_of(args, geo, c + threadIdx.x);
+    const long long u = head_units(geo, s, lane);
+    mine_units = u;
+    mine = u * geo.Hkv;
+    total += mine;
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+  if (lane == 0) sm.scan[warp] = total;
+  if (threadIdx.x == 0) sm.start_b = -1;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) total += sm.scan[w];
+  const long long run = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinUnits));
+  const long long u_begin = blockIdx.x * run, u_end = min(total, u_begin + run);
+  if (u_begin < u_end) {
+    long long before = 0;  // units of the chunks already walked
+    for (int c = 0; c < geo.B; c += NUM_THREADS) {
+      if (geo.B > NUM_THREADS) {
+        Seq s{0, 0, 0};
+        if (c + static_cast<int>(threadIdx.x) < geo.B) s = seq_of(args, geo, c + threadIdx.x);
+        const long long u = head_units(geo, s, lane);
+        mine_units = u;
+        mine = u * geo.Hkv;
+      }
+      long long inc = mine;  // inclusive scan over the block
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, inc, x);
+        if (lane >= x) inc += o;
+      }
+      __syncthreads();
+      if (lane == 31) sm.scan[warp] = inc;
+      __syncthreads();
+      long long prior = before, chunk = 0;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) prior += sm.scan[w];
+        chunk += sm.scan[w];
+      }
+      const long long end = prior + inc, first = end - mine;
+      if (first <= u_begin && u_begin < end) {
+        sm.start_b = c + threadIdx.x;
+        sm.start_unit = first;
+        sm.start_units = mine_units;
+      }
+      before += chunk;
+      if (before > u_begin) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort_flag = &sm.abort_flag;
+  Pieces pieces{&sm, abort_flag};
+
+  if (wg == 3) {
+    regs_dec<kOtherRegs>();
+    if (warp == PLAN_WARP) {
+      // ---------------------------------------------------------- planner
+      // Walks the run item by item and hands out its pieces.
+      ExtendDesc open{0, 0, 0, -1};  // the item that begins here and ends in another CTA
+      int ip = 0;                    // pieces handed out
+      auto hand_out = [&](const Piece& p) {
+        const int s = ip % NP;
+        if (ip >= NP && !mbar_wait_warp(smem_u32(&sm.piece_empty[s]), ((ip / NP) - 1) & 1, abort_flag)) return false;
+        if (lane == 0) {
+          sm.piece[s] = p;
+          mbar_arrive(smem_u32(&sm.piece_full[s]));
+        }
+        __syncwarp();
+        ++ip;
+        return true;
+      };
+      bool ok = true;
+      if (u_begin < u_end && sm.start_b >= 0) {
+        int b = sm.start_b;
+        Seq s = seq_of(args, geo, b);
+        const long long into = u_begin - sm.start_unit;
+        int h = static_cast<int>(into / sm.start_units);
+        // The item of key head h in which the run starts, 32 items at a time.
+        long long rem = into % sm.start_units;
+        int p = 0, lo, hi;
+        for (const int np = items_of(geo, s.nq); p < np; p += 32) {
+          int inc = p + lane < np ? 1 + item_tiles(geo, s, p + lane, lo, hi) : 0;
+          const int own = inc;
+#pragma unroll
+          for (int x = 1; x < 32; x <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc, x);
+            if (lane >= x) inc += o;
+          }
+          const unsigned past = __ballot_sync(0xffffffffu, inc > rem);
+          if (past) {
+            const int at = __ffs(past) - 1;
+            rem -= __shfl_sync(0xffffffffu, inc - own, at);
+            p += at;
+            break;
+          }
+          rem -= __shfl_sync(0xffffffffu, inc, 31);
+        }
+        long long u0 = u_begin - rem;  // the item's first unit
+        while (ok && u0 < u_end) {
+          const int nt = item_tiles(geo, s, p, lo, hi);
+          // Tile k of the item is unit u0 + 1 + k; the item's own unit u0 only says who
+          // writes an item without keys.
+          const int k0 = static_cast<int>(max(0LL, u_begin - u0 - 1)), k1 = static_cast<int>(min(static_cast<long long>(nt), u_end - u0 - 1));
+          if (k0 < k1 || (nt == 0 && u0 >= u_begin)) {
+            Piece w;
+            const int i0 = p * 2 * geo.tpt;
+            w.tok0 = s.tok0 + i0;
+            w.ntok = min(s.nq - i0, 2 * geo.tpt);
+            w.pos0 = s.n - s.nq + i0;
+            w.kvh = h;
+            w.b = b;
+            w.j0 = nt ? lo / BN + k0 : 0;
+            w.j1 = nt ? lo / BN + k1 : 0;
+            w.key_lo = lo;
+            w.key_hi = hi;
+            w.slot = k0 == 0 && k1 == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (k0 == 0 ? 1 : 0);
+            w.stop = 0;
+            w.pad = 0;
+            if (k0 == 0 && k1 < nt) open = ExtendDesc{w.tok0, w.ntok, h, static_cast<int>((u0 + nt) / run)};
+            ok = hand_out(w);
+          }
+          u0 += 1 + nt;
+          if (++p >= items_of(geo, s.nq)) {
+            p = 0;
+            if (++h >= geo.Hkv) {
+              h = 0;
+              do {
+                if (++b >= geo.B) break;
+                s = seq_of(args, geo, b);
+              } while (s.nq == 0);
+              if (b >= geo.B) break;
+            }
+          }
+        }
+      }
+      if (ok) {
+        Piece w{};
+        w.stop = 1;
+        hand_out(w);
+      }
+      if (lane == 0) args.desc[blockIdx.x] = open;
+    } else if (warp == Q_WARP) {
+      // ---------------------------------------------------------- Q loader
+      int nq[2] = {0, 0};
+      bool ok = true;
+      Piece p;
+      while (ok && pieces.next(p, lane)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          // A one-tile item's two slots share the Q tile of slot 0.
+          if (!slot_tiles(geo, p, t).any() || (t == 1 && one_tile(geo, p))) continue;
+          if (nq[t] > 0) ok = ok && mbar_wait_warp(smem_u32(&sm.q_empty[t]), (nq[t] - 1) & 1, abort_flag);
+          if (!ok) break;
+          if (lane == 0) {
+            const int tokens = min(p.ntok - t * geo.tpt, geo.tpt);
+            const int boxes = (tokens + q_box_tokens - 1) / q_box_tokens;
+            const uint32_t bar = smem_u32(&sm.q_full[t]);
+            const int rows = q_box_tokens * geo.G;
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * rows * 256));
+            for (int i = 0; i < boxes; ++i) {
+              const uint32_t dst = smem_u32(sm.q[t]) + i * rows * 128;
+              const int tok = p.tok0 + t * geo.tpt + i * q_box_tokens;
+              tma_load_3d(dst, &tm_q, bar, 0, p.kvh * geo.G, tok);
+              tma_load_3d(dst + HALF_BYTES, &tm_q, bar, 64, p.kvh * geo.G, tok);
+            }
+          }
+          __syncwarp();
+          ++nq[t];
+        }
+      }
+      for (int t = 0; t < 2; ++t)
+        if (nq[t] > 0) mbar_wait_drain(smem_u32(&sm.q_full[t]), (nq[t] - 1) & 1);
+    } else if (warp == KV_WARP) {
+      // ---------------------------------------------------------- K/V producer
+      // Lane l loads the tile's blocks l, l + 32, ...: each is one box per half of K and
+      // of V.  A tile's block-table entries are fetched one tile ahead (across items too),
+      // so that no load waits for them.
+      const int bs = 1 << args.block_shift;
+      const int rows = min(bs, BN);          // keys per box
+      const int nblk = BN / rows;            // boxes per tile and half: 1 .. 128
+      Piece p;
+      int ids[4], ids_next[4];
+      unsigned want = 0, want_next = 0;  // bit i: block lane + 32 i of the tile holds keys of the item
+      auto lookup = [&](const Piece& w, int j, int (&out)[4]) {
+        unsigned wanted = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int blk = lane + 32 * i;
+          const int key = j * BN + blk * rows;
+          out[i] = 0;
+          if (blk < nblk && key < w.key_hi && key + rows > w.key_lo) {
+            wanted |= 1u << i;
+            out[i] = args.block_table[static_cast<long long>(w.b) * args.max_blocks + (key >> args.block_shift)];
+          }
+        }
+        return wanted;
+      };
+      int kvi = 0;  // ring fills so far
+      bool ok = true, more = pieces.next(p, lane);
+      while (more && p.j0 == p.j1) more = pieces.next(p, lane);  // items without keys
+      int j = 0;
+      if (more) {
+        j = p.j0;
+        want = lookup(p, j, ids);
+      }
+      while (ok && more) {
+        // The tile after this one.
+        Piece pn = p;
+        int jn = j + 1;
+        bool more_n = true;
+        if (jn == p.j1) {
+          do more_n = pieces.next(pn, lane);
+          while (more_n && pn.j0 == pn.j1);
+          jn = pn.j0;
+        }
+        if (more_n) want_next = lookup(pn, jn, ids_next);
+
+        const int y = (j * BN) & (bs - 1) & ~(rows - 1);
+        uint32_t bad[4] = {0u, 0u, 0u, 0u};
+        bool any_bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!(want >> i & 1u) || (ids[i] >= 0 && ids[i] < args.num_blocks)) continue;
+          want &= ~(1u << i);
+          any_bad = true;
+          const int k0 = (lane + 32 * i) * rows;  // the block's keys, a run inside a word or whole words
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            if (rows >= 32 ? (w >= k0 / 32 && w < (k0 + rows) / 32) : w == k0 / 32)
+              bad[w] |= rows >= 32 ? 0xffffffffu : ((1u << rows) - 1u) << (k0 & 31);
+        }
+        if (__any_sync(0xffffffffu, any_bad)) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) bad[w] = __reduce_or_sync(0xffffffffu, bad[w]);
+          if (lane == 0) atomicOr(&g_status, kStatusBadBlock);
+        }
+        const uint32_t bytes = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(want))) * rows * 256u;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int s = kvi % NS;
+          if (kvi >= NS) ok = mbar_wait_warp(smem_u32(&sm.kv_empty[s]), ((kvi / NS) - 1) & 1, abort_flag);
+          if (!ok) break;
+          const uint32_t bar = smem_u32(&sm.kv_full[s]);
+          if (lane == 0) {
+            // The tile four before is done with these words: the V tile filled last took the
+            // place of that of three tiles before this one, whose PV was complete.
+            if (v == 0)
+              for (int w = 0; w < 4; ++w) sm.bad[(kvi >> 1) & 3][w] = bad[w];
+            mbar_arrive_expect_tx(bar, bytes);
+          }
+          __syncwarp();
+          const CUtensorMap* tm = v ? &tm_v : &tm_k;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (want >> i & 1u) {
+              const uint32_t dst = smem_u32(sm.kv[s]) + (lane + 32 * i) * rows * 128;
+              const int z = ids[i] * geo.Hkv + p.kvh;
+              tma_load_3d(dst, tm, bar, 0, y, z);
+              tma_load_3d(dst + HALF_BYTES, tm, bar, 64, y, z);
+            }
+          __syncwarp();
+          ++kvi;
+        }
+        p = pn;
+        j = jn;
+        more = more_n;
+        want = want_next;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ids[i] = ids_next[i];
+      }
+      for (int i = max(0, kvi - NS); i < kvi; ++i) mbar_wait_drain(smem_u32(&sm.kv_full[i % NS]), (i / NS) & 1);
+    } else {
+      // ---------------------------------------------------------- MMA issuer
+      // The whole warp runs this (warp-uniform waits); MMAs and commits go out from one
+      // elected lane.
+      int base = 0;           // key tiles of the pieces before this one (ring position / 2)
+      // Phase bits, bit t for slot t: Q_PH q_full, P_PH p_full and O_PH o_free to wait for
+      // next; O_USED: an item has used O_t; Q_HERE: the item's Q tile has landed.
+      enum : uint32_t { Q_PH = 0, P_PH = 2, O_PH = 4, O_USED = 6, Q_HERE = 8 };
+      uint32_t ph = 0;
+      auto bit = [&](uint32_t i) { return (ph >> i) & 1u; };
+      bool ok = true;
+      Piece p;
+      while (ok && pieces.next(p, lane)) {
+        const int nt = p.j1 - p.j0;
+        if (nt == 0) continue;
+        ph &= ~(3u << Q_HERE);
+        const int k0 = 2 * (base - p.j0);  // ring entries of tile j: K k0 + 2 j, V the next
+        auto addr = [&](int i) { return smem_u32(sm.kv[i % NS]); };
+        auto wait_kv = [&](int i) {
+          return mbar_wait_warp(smem_u32(&sm.kv_full[i % NS]), static_cast<uint32_t>((i / NS) & 1), abort_flag);
+        };
+        auto free_kv = [&](int i) { commit_elect(smem_u32(&sm.kv_empty[i % NS])); };
+        // S_t of key tile j from Q slot qs; `last`: the item's last use of that slot.
+        auto issue_s = [&](int t, int qs, int j, bool last) {
+          if (!bit(Q_HERE + qs)) {
+            if (!mbar_wait_warp(smem_u32(&sm.q_full[qs]), bit(Q_PH + qs), abort_flag)) return false;
+            ph ^= 1u << (Q_PH + qs);
+            ph |= 1u << (Q_HERE + qs);
+          }
+          issue_qk<T>(tmem + 128 * t, smem_u32(sm.q[qs]), addr(k0 + 2 * j));
+          commit_elect(smem_u32(&sm.s_full[t]));
+          if (last) commit_elect(smem_u32(&sm.q_empty[qs]));
+          return true;
+        };
+        // PV_t of key tile j, once P is there.  The slot's first overwrites O_t (which the
+        // epilogue must have read out), its last publishes it.
+        auto issue_o = [&](int t, int j, bool first, bool last) {
+          if (first && bit(O_USED + t)) {
+            if (!mbar_wait_warp(smem_u32(&sm.o_free[t]), bit(O_PH + t), abort_flag)) return false;
+            ph ^= 1u << (O_PH + t);
+          }
+          if (!mbar_wait_warp(smem_u32(&sm.p_full[t]), bit(P_PH + t), abort_flag)) return false;
+          ph ^= 1u << (P_PH + t);
+          tc_fence_after();
+          issue_pv<T>(tmem + 256 + 128 * t, tmem + 128 * t, addr(k0 + 2 * j + 1), first ? 0u : 1u);
+          if (last) {
+            commit_elect(smem_u32(&sm.o_full[t]));
+            ph |= 1u << (O_USED + t);
+          }
+          return true;
+        };
+        // V_j has landed; its rows without a key of the item are cleared.
+        auto ready_v = [&](int j) {
+          if (!wait_kv(k0 + 2 * j + 1)) return false;
+          const uint32_t* bad = sm.bad[(k0 / 2 + j) & 3];
+          const int lo = p.key_lo - j * BN, hi = p.key_hi - j * BN;
+          if (lo > 0 || hi < BN || (bad[0] | bad[1] | bad[2] | bad[3]) != 0u)
+            zero_v_rows(addr(k0 + 2 * j + 1), lo, hi, bad, lane);
+          return true;
+        };
+        if (one_tile(geo, p)) {
+          // Slots take turns: S of tile j + 2 follows PV of tile j in the same slot.
+          for (int j = p.j0; ok && j < min(p.j1, p.j0 + 2); ++j) {
+            ok = wait_kv(k0 + 2 * j) && issue_s(j - p.j0, 0, j, j == p.j1 - 1);
+            if (ok) free_kv(k0 + 2 * j);
+          }
+          for (int j = p.j0; ok && j < p.j1; ++j) {
+            const int t = (j - p.j0) & 1;
+            const bool next = j + 2 < p.j1;
+            ok = ready_v(j) && (!next || wait_kv(k0 + 2 * j + 4)) && issue_o(t, j, j < p.j0 + 2, !next);
+            if (!ok) break;
+            free_kv(k0 + 2 * j + 1);
+            if (next) {
+              ok = issue_s(t, 0, j + 2, j + 2 == p.j1 - 1);
+              if (ok) free_kv(k0 + 2 * j + 4);
+            }
+          }
+        } else {
+          const Tiles t0 = slot_tiles(geo, p, 0), t1 = slot_tiles(geo, p, 1);
+          ok = wait_kv(k0 + 2 * p.j0);
+          if (ok && t0.has(p.j0)) ok = issue_s(0, 0, p.j0, p.j0 == t0.end - 1);
+          if (ok && t1.has(p.j0)) ok = issue_s(1, 1, p.j0, p.j0 == t1.end - 1);
+          if (ok) free_kv(k0 + 2 * p.j0);
+          for (int j = p.j0; ok && j < p.j1; ++j) {
+            const bool next = j + 1 < p.j1;
+            ok = ready_v(j) && (!next || wait_kv(k0 + 2 * j + 2));
+            if (ok && t0.has(j)) ok = issue_o(0, j, j == t0.first, j == t0.end - 1);
+            if (ok && next && t0.has(j + 1)) ok = issue_s(0, 0, j + 1, j + 1 == t0.end - 1);
+            if (ok && t1.has(j)) ok = issue_o(1, j, j == t1.first, j == t1.end - 1);
+            if (!ok) break;
+            free_kv(k0 + 2 * j + 1);
+            if (next) {
+              if (t1.has(j + 1)) ok = issue_s(1, 1, j + 1, j + 1 == t1.end - 1);
+              if (ok) free_kv(k0 + 2 * j + 2);
+            }
+          }
+        }
+        base += nt;
+      }
+      // All MMAs issued by this warp must complete before TMEM is freed.
+      commit_elect(smem_u32(&sm.mma_done));
+      mbar_wait_drain(smem_u32(&sm.mma_done), 0);
+      __syncwarp();
+    }
+  } else if (wg == EPI_WG) {
+    // ------------------------------------------------------------ epilogue
+    // Thread = one row of a tile.  O comes out of TMEM 16 columns at a time, is scaled
+    // (and, for a one-tile item, the two slots' states are joined), staged in the warp's
+    // own 4 KB and written in runs of 128 bytes a row: 16-bit O, or float32 partials.
+    regs_dec<kEpilogueRegs>();
+    const int wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const int row_tok = row / geo.G, row_head = row - row_tok * geo.G;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t stage = smem_u32(sm.stage[wq]);
+    int nfull[2] = {0, 0};
+    bool ok = true;
+    Piece p;
+    while (ok && pieces.next(p, lane)) {
+      const bool single = one_tile(geo, p);
+      for (int t = 0; t < (single ? 1 : 2) && ok; ++t) {
+        const int nrows = tile_rows(geo, p, t);
+        const bool valid = row < nrows;
+        const long long out_row =
+            static_cast<long long>(p.tok0 + t * geo.tpt + row_tok) * geo.Hq + p.kvh * geo.G + row_head;
+        const long long part_row = p.slot < 0 ? 0 : static_cast<long long>(p.slot) * args.slot_rows + t * BM + row;
+        const bool on = slot_tiles(geo, p, t).any();
+        const bool both = single && slot_tiles(geo, p, 1).any();
+        if (!on) {
+          // No key tile: a whole item's rows see nothing; a piece adds nothing.
+          if (valid) {
+            if (p.slot >= 0) {
+              args.ws_lse[part_row] = -INFINITY;
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.o) + out_row * D);
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (args.lse != nullptr) args.lse[out_row] = -INFINITY;
+            }
+          }
+          continue;
+        }
+        ok = mbar_wait_warp(smem_u32(&sm.o_full[t]), nfull[t] & 1, abort_flag) &&
+             mbar_wait_warp(smem_u32(&sm.st_full[t]), nfull[t] & 1, abort_flag);
+        if (ok && both)
+          ok = mbar_wait_warp(smem_u32(&sm.o_full[1]), nfull[1] & 1, abort_flag) &&
+               mbar_wait_warp(smem_u32(&sm.st_full[1]), nfull[1] & 1, abort_flag);
+        if (!ok) break;
+        ++nfull[t];
+        if (both) ++nfull[1];
+        tc_fence_after();
+        float m = sm.stat_m[t][row], l = sm.stat_l[t][row];
+        mbar_arrive(smem_u32(&sm.st_empty[t]));
+        float f0 = 1.f, f1 = 0.f;
+        if (both) {
+          const float m1 = sm.stat_m[1][row], l1 = sm.stat_l[1][row];
+          mbar_arrive(smem_u32(&sm.st_empty[1]));
+          const float mm = fmaxf(m, m1);
+          f0 = m == -INFINITY ? 0.f : ex2_approx((m - mm) * args.scale_log2);
+          f1 = m1 == -INFINITY ? 0.f : ex2_approx((m1 - mm) * args.scale_log2);
+          l = f0 * l + f1 * l1;
+          m = mm;
+        }
+        // l > 0: the row saw keys; l = 0: none; NaN marks a NaN score.
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const bool none = l == 0.f;
+        f0 *= inv;
+        f1 *= inv;
+        const uint32_t tO = tmem + lane_off + 256 + t * 128;
+        const bool part = p.slot >= 0;
+        // 16 columns per step; four steps (16-bit) or two (float32) fill 128 bytes a row.
+        const int steps = part ? 2 : 4;
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          FA_TMEM_LD16(tO + 16 * c, o);
+          if (both) {
+            uint32_t o1[16];
+            FA_TMEM_LD16(tO + 128 + 16 * c, o1);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e]) * f0));
+          } else {
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+          }
+          if (c == D / 16 - 1) {
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sm.o_free[t]));
+            if (both) mbar_arrive(smem_u32(&sm.o_free[1]));
+          }
+          if (none) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0u;
+          }
+          const int step = c & (steps - 1);
+          if (step == 0) __syncwarp();  // the stage's last rows have been read
+          if (part) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const uint32_t dst = stage + lane * 128 + (((4 * step + v) ^ (lane & 7)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(o[4 * v]), "r"(o[4 * v + 1]),
+                           "r"(o[4 * v + 2]), "r"(o[4 * v + 3])
+                           : "memory");
+            }
+          } else {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const uint32_t dst = stage + lane * 128 + (((2 * step + v) ^ (lane & 7)) << 4);
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = pack2<T>(__uint_as_float(o[8 * v + 2 * i]), __uint_as_float(o[8 * v + 2 * i + 1]));
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            }
+          }
+          if (step == steps - 1) {
+            __syncwarp();
+            // Eight lanes a row, four rows a step.
+            char* out = part ? reinterpret_cast<char*>(args.ws_o) : static_cast<char*>(args.o);
+            const long long my_byte = part ? part_row * (D * 4) + (c / 2) * 128 : out_row * (D * 2) + (c / 4) * 128;
+#pragma unroll 1
+            for (int r = 0; r < 32; r += 4) {
+              if (wq * 32 + r >= nrows) break;
+              const int rr = r + (lane >> 3), ch = lane & 7;
+              const long long at = __shfl_sync(0xffffffffu, my_byte, rr);
+              uint4 v;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                           : "r"(stage + rr * 128 + ((ch ^ (rr & 7)) << 4)));
+              if (wq * 32 + rr < nrows) *reinterpret_cast<uint4*>(out + at + ch * 16) = v;
+            }
+          }
+        }
+        if (valid) {
+          const float lse = l > 0.f ? m * args.scale + logf(l) : (none ? -INFINITY : l);
+          if (part)
+            args.ws_lse[part_row] = lse;
+          else if (args.lse != nullptr)
+            args.lse[out_row] = lse;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax warps
+    // Warpgroup t is the softmax of slot t: thread = row, all 128 score columns of a key
+    // tile in registers (as in fwd_tc.cu).  A warp without a valid row only keeps step.
+    regs_inc<kSoftmaxRegs>();
+    const int t = wg;
+    const int wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const int row_tok = row / geo.G;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_off + t * 128;
+    const uint32_t tO = tmem + lane_off + 256 + t * 128;
+    const float sl2 = args.scale_log2;
+    int ns = 0;    // S tiles consumed
+    int nst = 0;   // items published
+    int base = 0;  // key tiles of the pieces before this one
+    bool ok = true;
+    Piece p;
+    while (ok && pieces.next(p, lane)) {
+      const Tiles my = slot_tiles(geo, p, t);
+      const int tbase = base - p.j0;
+      base += p.j1 - p.j0;
+      if (!my.any()) continue;
+      const bool single = one_tile(geo, p);
+      const int rt = single ? 0 : t;  // the slot's row tile
+      const int nrows = tile_rows(geo, p, rt);
+      const bool busy = wq * 32 < nrows;
+      const int p_first = p.pos0 + rt * geo.tpt;                           // positions of the tile's first
+      const int p_last = p_first + min(p.ntok - rt * geo.tpt, geo.tpt) - 1;  // and last token
+      const int row_p = p_first + row_tok;
+      float m = -INFINITY, l = 0.f;
+      bool nan_row = false;
+      for (int j = my.first; j < my.end; j += my.step, ++ns) {
+        ok = mbar_wait_warp(smem_u32(&sm.s_full[t]), ns & 1, abort_flag);
+        if (!ok) break;
+        if (!busy) {
+          mbar_arrive(smem_u32(&sm.p_full[t]));
+          continue;
+        }
+        tc_fence_after();
+        const int kb = j * BN;
+        const uint4 bad = *reinterpret_cast<const uint4*>(sm.bad[(tbase + j) & 3]);
+        const bool any_bad = (bad.x | bad.y | bad.z | bad.w) != 0u;
+        if (kb + BN > p.key_hi || kb < p.key_lo || (geo.causal && kb + BN - 1 > p_first) ||
+            (geo.window > 0 && kb <= p_last - geo.window) || any_bad) {
+          // Visible keys of this row: columns [c_lo, c_hi), without the blocks outside the pool.
+          int c_hi = min(BN, p.key_hi - kb), c_lo = max(0, p.key_lo - kb);
+          if (geo.causal) c_hi = min(c_hi, row_p - kb + 1);
+          if (geo.window > 0) c_lo = max(c_lo, row_p - geo.window + 1 - kb);
+          c_hi = max(c_hi, c_lo);
+#pragma unroll 1
+          for (int c = 0; c < BN / 32; ++c) {
+            const uint32_t bw = c == 0 ? bad.x : c == 1 ? bad.y : c == 2 ? bad.z : bad.w;
+            if (bw == 0u && __all_sync(0xffffffffu, c_lo <= 32 * c && c_hi >= 32 * c + 32)) continue;
+            uint32_t r[32];
+            if (__all_sync(0xffffffffu, c_hi <= 32 * c || c_lo >= 32 * c + 32)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(-INFINITY);
+            } else {
+              FA_TMEM_LD32(tS + 32 * c, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = keep_or_ninf(r[e], 32 * c + e, c_lo, c_hi);
+              if (bw != 0u) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = (bw >> e) & 1u ? __float_as_uint(-INFINITY) : r[e];
+              }
+            }
+            FA_TMEM_ST32(tS + 32 * c, r);
+          }
+          tmem_st_wait();
+        }
+        uint32_t s[BN];
+        FA_TMEM_LD32(tS + 0, (s + 0));
+        FA_TMEM_LD32(tS + 32, (s + 32));
+        FA_TMEM_LD32(tS + 64, (s + 64));
+        FA_TMEM_LD32(tS + 96, (s + 96));
+        tmem_ld_wait();
+        float mm[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          mm[q] = fmax3_nan(__uint_as_float(s[q]), __uint_as_float(s[q + 8]), -INFINITY);
+#pragma unroll
+        for (int c = 16; c < BN; c += 16)
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            mm[q] = fmax3_nan(mm[q], __uint_as_float(s[c + q]), __uint_as_float(s[c + 8 + q]));
+        const float mx = fmax3_nan(fmax3_nan(mm[0], mm[1], mm[2]), fmax3_nan(mm[3], mm[4], mm[5]),
+                                   fmax3_nan(mm[6], mm[7], -INFINITY));
+        nan_row |= (mx != mx);
+        const float m_new = fmaxf(m, mx);
+        const bool need = (m_new - m) * sl2 > kRescaleThreshold;
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2_approx((m - m_new) * sl2);
+          m = m_new;
+          l *= alpha;
+        }
+        if (j > my.first && __any_sync(0xffffffffu, need)) {
+          // O_t's last update is complete: S_t of this tile was issued after it.
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t r[32];
+            FA_TMEM_LD32(tO + 32 * c, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+            FA_TMEM_ST32(tO + 32 * c, r);
+          }
+        }
+        const float ms = (m == -INFINITY) ? 0.f : m * sl2;
+        const uint64_t sl2x2 = f2_pack(sl2, sl2), nms2 = f2_pack(-ms, -ms);
+        uint64_t acc[4] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(s[32 * c + e]), __uint_as_float(s[32 * c + e + 1])),
+                                       sl2x2, nms2);
+            float x0, x1;
+            f2_unpack(x2, x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            acc[(e >> 1) & 3] = f2_add(acc[(e >> 1) & 3], f2_pack(p0, p1));
+            // P in 16 bits, the MMA's type: relative error 2^-9 (bf16) a weight, below the
+            // output's own rounding after the sum; l adds the unrounded values.
+            pk[e >> 1] = pack2<T>(p0, p1);
+          }
+          asm volatile(
+              "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+                  tS + 16 * c),
+              "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]),
+              "r"(pk[8]), "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]), "r"(pk[14]), "r"(pk[15])
+              : "memory");
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sm.p_full[t]));
+        {
+          const uint64_t s01 = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
+          float a0, a1;
+          f2_unpack(s01, a0, a1);
+          l += a0 + a1;
+        }
+      }
+      if (!ok) break;
+      if (nst > 0) ok = mbar_wait_warp(smem_u32(&sm.st_empty[t]), (nst - 1) & 1, abort_flag);
+      if (!ok) break;
+      sm.stat_m[t][row] = m;
+      sm.stat_l[t][row] = nan_row ? __uint_as_float(0x7fc00000u) : l;
+      mbar_arrive(smem_u32(&sm.st_full[t]));
+      ++nst;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partial results of an item that several CTAs share: with lse_s of piece s,
+// lse = ln sum exp(lse_s), o = sum exp(lse_s - lse) o_s.  One warp per row; block x
+// looks at the item that begins in CTA x and ends in a later one, if there is one.
+constexpr int CB_WARPS = 8;
+template <class T>
+__global__ void __launch_bounds__(CB_WARPS * 32) combine_kernel(const __grid_constant__ ExtendArgs args) {
+  const ExtendDesc d = args.desc[blockIdx.x];
+  if (d.last < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int G = args.Hq / args.Hkv, tpt = BM / G;
+  const int first = blockIdx.x, pieces = d.last - first + 1;
+  for (int r = blockIdx.y * CB_WARPS + (threadIdx.x >> 5); r < d.ntok * G; r += gridDim.y * CB_WARPS) {
+    const int tok = r / G, head = r - tok * G;
+    const int t = tok >= tpt ? 1 : 0;
+    const int srow = t * BM + r - t * tpt * G;  // the row's place in a slot
+    auto row_of = [&](int s) {
+      return static_cast<long long>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * args.slot_rows + srow;
+    };
+    float M = -INFINITY;
+    for (int s = lane; s < pieces; s += 32) {
+      const float v = args.ws_lse[row_of(s)];
+      M = M != M || v != v ? __uint_as_float(0x7fc00000u) : fmaxf(M, v);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) {
+      const float v = __shfl_xor_sync(0xffffffffu, M, x);
+      M = M != M || v != v ? __uint_as_float(0x7fc00000u) : fmaxf(M, v);
+    }
+    float W = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (M != -INFINITY) {
+      for (int s0 = 0; s0 < pieces; s0 += 32) {
+        const float w_l = s0 + lane < pieces ? __expf(args.ws_lse[row_of(s0 + lane)] - M) : 0.f;
+        const int n = min(32, pieces - s0);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+          const float w = __shfl_sync(0xffffffffu, w_l, i);
+          if (w == 0.f) continue;  // a piece without a visible key wrote no o
+          const float4 v = *reinterpret_cast<const float4*>(args.ws_o + row_of(s0 + i) * D + lane * 4);
+          W += w;
+          acc.x = fmaf(w, v.x, acc.x);
+          acc.y = fmaf(w, v.y, acc.y);
+          acc.z = fmaf(w, v.z, acc.z);
+          acc.w = fmaf(w, v.w, acc.w);
+        }
+      }
+    }
+    const float inv = W == 0.f ? 0.f : 1.f / W;  // a NaN logsumexp makes the row NaN
+    const long long out = static_cast<long long>(d.tok0 + tok) * args.Hq + d.kvh * G + head;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.o) + out * D + lane * 4) =
+        make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+    if (lane == 0 && args.lse != nullptr) args.lse[out] = W == 0.f ? -INFINITY : M + logf(W);
+  }
+}
+
+}  // namespace ext
+
+cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
+  using namespace ext;
+  const int G = a.Hq / a.Hkv, tpt = BM / G;
+  // Q boxes: the largest divisor of a tile's tokens that keeps a box within 32 rows.
+  int box = 1;
+  for (int i = 1; i <= tpt; ++i)
+    if (tpt % i == 0 && i * G <= 32) box = i;
+  const int bs = 1 << a.block_shift;
+  CUtensorMap tq, tk, tv;
+  const long long qd[3] = {D, a.Hq, a.T}, qs[2] = {D * 2, a.q_stride * 2};
+  const int qb[3] = {64, G, box};
+  const long long pd[3] = {D, bs, static_cast<long long>(a.num_blocks) * a.Hkv}, ps[2] = {D * 2, static_cast<long long>(bs) * D * 2};
+  const int pb[3] = {64, bs < BN ? bs : BN, 1};
+  if (!make_tmap_3d_half(&tq, a.q, qd, qs, qb, a.f16) || !make_tmap_3d_half(&tk, a.kpool, pd, ps, pb, a.f16) ||
+      !make_tmap_3d_half(&tv, a.vpool, pd, ps, pb, a.f16))
+    return cudaErrorInvalidValue;
+  auto kernel = a.f16 ? extend_kernel<F16> : extend_kernel<Bf16>;
+  // With fewer registers than the split draws on, setmaxnreg.inc would wait forever.
+  cudaFuncAttributes fattr{};
+  cudaError_t e = cudaFuncGetAttributes(&fattr, reinterpret_cast<const void*>(kernel));
+  if (e != cudaSuccess) return e;
+  if (fattr.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+  e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmemBytes);
+  if (e != cudaSuccess) return e;
+  int sms = 0;
+  e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(sms < kExtendMaxCtas ? sms : kExtendMaxCtas);
+  kernel<<<grid, NUM_THREADS, kSmemBytes, stream>>>(tq, tk, tv, a, box);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const dim3 cgrid(grid, (a.slot_rows + CB_WARPS * 4 - 1) / (CB_WARPS * 4));
+  (a.f16 ? combine_kernel<F16> : combine_kernel<Bf16>)<<<cgrid, CB_WARPS * 32, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t take_status_extend(unsigned int* out) { return take_local_status(out); }
+
+}  // namespace fa
