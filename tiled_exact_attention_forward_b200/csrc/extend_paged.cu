@@ -38,7 +38,7 @@ namespace ext {
 constexpr int BM = 128;                     // rows per tile
 constexpr int BN = 128;                     // keys per tile
 constexpr int D = 128;
-constexpr int NS = 4;                       // K/V ring stages (K and V tiles interleaved)
+constexpr int NS = 2;                       // stages of the K ring and of the V ring
 constexpr int TILE_BYTES = BM * D * 2;
 constexpr int HALF_BYTES = TILE_BYTES / 2;  // one 64-column half (128-byte rows, swizzled)
 constexpr int NUM_THREADS = 512;
@@ -46,11 +46,11 @@ constexpr int WARPS = NUM_THREADS / 32;
 constexpr int WG_THREADS = 128;
 constexpr int EPI_WG = 2;
 constexpr int MMA_WARP = 12;
-constexpr int KV_WARP = 13;
-constexpr int Q_WARP = 14;
+constexpr int K_WARP = 13;                  // Q and K tiles
+constexpr int V_WARP = 14;                  // V tiles
 constexpr int PLAN_WARP = 15;
-constexpr int NP = 4;                       // pieces in flight between the planner and the other warps
-constexpr int kPieceReaders = 15;           // warps that read a piece: MMA, K/V, Q, 8 softmax, 4 epilogue
+constexpr int NP = 8;                       // pieces in flight between the planner and the other warps
+constexpr int kPieceReaders = 15;           // warps that read a piece: MMA, K, V, 8 softmax, 4 epilogue
 constexpr int kSoftmaxRegs = 192;
 constexpr int kEpilogueRegs = 64;
 constexpr int kOtherRegs = 64;
@@ -77,13 +77,15 @@ struct Piece {
 
 struct Smem {
   uint8_t q[2][TILE_BYTES];
-  uint8_t kv[NS][TILE_BYTES];
+  uint8_t k[NS][TILE_BYTES];
+  uint8_t v[NS][TILE_BYTES];
   uint8_t stage[4][HALF_BYTES / 4];  // epilogue, per warp: 32 rows of 128 bytes
   uint32_t bad[4][BN / 32];          // keys of a tile whose block lies outside the pool
   Piece piece[NP];
   uint64_t piece_full[NP], piece_empty[NP];
   uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[NS], kv_empty[NS];
+  uint64_t k_full[NS], k_empty[NS];
+  uint64_t v_full[NS], v_empty[NS];
   uint64_t s_full[2];
   uint64_t p_full[2];
   uint64_t o_full[2], o_free[2];
@@ -185,6 +187,15 @@ __device__ __forceinline__ int tile_rows(const Geo& g, const Piece& p, int t) {
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
 __host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
 
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ void commit_elect(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -213,20 +224,22 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
         "=r"(r[14]), "=r"(r[15])                                                                     \
       : "r"(taddr))
 
-// A warp's view of the planner's ring of pieces.
+// A warp's view of the planner's ring of pieces.  Pieces stay in shared memory until the
+// warp releases them: what a role needs of one now and then is read there, since a
+// spilled register costs a local load, and with this much shared memory in use little
+// L1 is left to catch it (measured: 60 bytes of spills in the MMA and producer warps
+// took a quarter of the kernel's time).
 struct Pieces {
   Smem* sm;
   volatile int* abort_flag;
-  int i = 0;
-  // The next piece; false at the end (or when the CTA gives up).
-  __device__ __forceinline__ bool next(Piece& p, int lane) {
-    const int s = i % NP;
-    if (!mbar_wait_warp(smem_u32(&sm->piece_full[s]), (i / NP) & 1, abort_flag)) return false;
-    p = sm->piece[s];
+  __device__ __forceinline__ const Piece& at(int i) const { return sm->piece[i % NP]; }
+  // Waits for piece i; false at the end (or when the CTA gives up).
+  __device__ __forceinline__ bool wait(int i) const {
+    return mbar_wait_warp(smem_u32(&sm->piece_full[i % NP]), (i / NP) & 1, abort_flag) && !at(i).stop;
+  }
+  __device__ __forceinline__ void release(int i, int lane) const {
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm->piece_empty[s]));
-    ++i;
-    return !p.stop;
+    if (lane == 0) mbar_arrive(smem_u32(&sm->piece_empty[i % NP]));
   }
 };
 
@@ -270,8 +283,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(smem_u32(&sm.st_empty[t]), WG_THREADS);
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_u32(&sm.kv_full[s]), 1);
-      mbar_init(smem_u32(&sm.kv_empty[s]), 1);
+      mbar_init(smem_u32(&sm.k_full[s]), 1);
+      mbar_init(smem_u32(&sm.k_empty[s]), 1);
+      mbar_init(smem_u32(&sm.v_full[s]), 1);
+      mbar_init(smem_u32(&sm.v_empty[s]), 1);
     }
     for (int s = 0; s < NP; ++s) {
       mbar_init(smem_u32(&sm.piece_full[s]), 1);
@@ -285,7 +300,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(smem_u32(&sm.tmem_base), 512);
     tmem_relinquish();
   }
-  if (warp == KV_WARP && lane == 0) {
+  if (warp == K_WARP && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -354,7 +369,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
-  Pieces pieces{&sm, abort_flag};
+  const Pieces pieces{&sm, abort_flag};
 
   if (wg == 3) {
     regs_dec<kOtherRegs>();
@@ -444,158 +459,163 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         hand_out(w);
       }
       if (lane == 0) args.desc[blockIdx.x] = open;
-    } else if (warp == Q_WARP) {
-      // ---------------------------------------------------------- Q loader
-      int nq[2] = {0, 0};
+    } else if (warp == K_WARP || warp == V_WARP) {
+      // ---------------------------------------------------------- K and Q, V producers
+      // A warp each, so that K tiles run ahead of the V tiles that wait for a softmax.
+      // Lane l holds the tile's block-table entries l, l + 32, ..., fetched one tile ahead
+      // (across items too); the boxes go out one after another from one elected lane.
+      const bool is_k = warp == K_WARP;
+      const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+      uint64_t* full = is_k ? sm.k_full : sm.v_full;
+      uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
+      const uint32_t ring = is_k ? smem_u32(sm.k[0]) : smem_u32(sm.v[0]);
+      const int rows = min(1 << args.block_shift, BN);  // keys per box
+      const int nblk = BN / rows;                       // blocks per tile: 1 .. 128
+      // Does block `blk` of tile j hold keys of the item?
+      auto wanted = [&](const Piece& w, int j, int blk) {
+        const int key = j * BN + blk * rows;
+        return blk < nblk && key < w.key_hi && key + rows > w.key_lo;
+      };
+      auto lookup = [&](const Piece& w, int j, int blk) {
+        return wanted(w, j, blk) ? args.block_table[static_cast<long long>(w.b) * args.max_blocks + ((j * BN + blk * rows) >> args.block_shift)] : 0;
+      };
+      int n = 0;           // tiles loaded so far
+      int np = 0;          // K: items started
+      int nq0 = 0, nq1 = 0;  // K: Q tiles loaded, per slot
       bool ok = true;
-      Piece p;
-      while (ok && pieces.next(p, lane)) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          // A one-tile item's two slots share the Q tile of slot 0.
-          if (!slot_tiles(geo, p, t).any() || (t == 1 && one_tile(geo, p))) continue;
-          if (nq[t] > 0) ok = ok && mbar_wait_warp(smem_u32(&sm.q_empty[t]), (nq[t] - 1) & 1, abort_flag);
-          if (!ok) break;
+      // The Q tiles of a new item.  A one-tile item uses one slot, in turn with the next
+      // one's, so that its Q tile is there before the last item is done with its own.
+      auto load_q = [&](const Piece& p) {
+        const bool single = one_tile(geo, p);
+        for (int t = 0; t < (single ? 1 : 2); ++t) {
+          if (!single && !slot_tiles(geo, p, t).any()) continue;
+          const int qs = single ? np & 1 : t;
+          const int used = qs ? nq1++ : nq0++;
+          if (used > 0) ok = ok && mbar_wait_warp(smem_u32(&sm.q_empty[qs]), (used - 1) & 1, abort_flag);
+          if (!ok) return;
           if (lane == 0) {
             const int tokens = min(p.ntok - t * geo.tpt, geo.tpt);
             const int boxes = (tokens + q_box_tokens - 1) / q_box_tokens;
-            const uint32_t bar = smem_u32(&sm.q_full[t]);
-            const int rows = q_box_tokens * geo.G;
-            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * rows * 256));
+            const uint32_t bar = smem_u32(&sm.q_full[qs]);
+            const int box_rows = q_box_tokens * geo.G;
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * box_rows * 256));
             for (int i = 0; i < boxes; ++i) {
-              const uint32_t dst = smem_u32(sm.q[t]) + i * rows * 128;
+              const uint32_t dst = smem_u32(sm.q[qs]) + i * box_rows * 128;
               const int tok = p.tok0 + t * geo.tpt + i * q_box_tokens;
               tma_load_3d(dst, &tm_q, bar, 0, p.kvh * geo.G, tok);
               tma_load_3d(dst + HALF_BYTES, &tm_q, bar, 64, p.kvh * geo.G, tok);
             }
           }
           __syncwarp();
-          ++nq[t];
         }
-      }
-      for (int t = 0; t < 2; ++t)
-        if (nq[t] > 0) mbar_wait_drain(smem_u32(&sm.q_full[t]), (nq[t] - 1) & 1);
-    } else if (warp == KV_WARP) {
-      // ---------------------------------------------------------- K/V producer
-      // Lane l loads the tile's blocks l, l + 32, ...: each is one box per half of K and
-      // of V.  A tile's block-table entries are fetched one tile ahead (across items too),
-      // so that no load waits for them.
-      const int bs = 1 << args.block_shift;
-      const int rows = min(bs, BN);          // keys per box
-      const int nblk = BN / rows;            // boxes per tile and half: 1 .. 128
-      Piece p;
-      int ids[4], ids_next[4];
-      unsigned want = 0, want_next = 0;  // bit i: block lane + 32 i of the tile holds keys of the item
-      auto lookup = [&](const Piece& w, int j, int (&out)[4]) {
-        unsigned wanted = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int blk = lane + 32 * i;
-          const int key = j * BN + blk * rows;
-          out[i] = 0;
-          if (blk < nblk && key < w.key_hi && key + rows > w.key_lo) {
-            wanted |= 1u << i;
-            out[i] = args.block_table[static_cast<long long>(w.b) * args.max_blocks + (key >> args.block_shift)];
-          }
-        }
-        return wanted;
+        ++np;
       };
-      int kvi = 0;  // ring fills so far
-      bool ok = true, more = pieces.next(p, lane);
-      while (more && p.j0 == p.j1) more = pieces.next(p, lane);  // items without keys
-      int j = 0;
-      if (more) {
-        j = p.j0;
-        want = lookup(p, j, ids);
-      }
-      while (ok && more) {
-        // The tile after this one.
-        Piece pn = p;
-        int jn = j + 1;
-        bool more_n = true;
-        if (jn == p.j1) {
-          do more_n = pieces.next(pn, lane);
-          while (more_n && pn.j0 == pn.j1);
-          jn = pn.j0;
-        }
-        if (more_n) want_next = lookup(pn, jn, ids_next);
-
-        const int y = (j * BN) & (bs - 1) & ~(rows - 1);
-        uint32_t bad[4] = {0u, 0u, 0u, 0u};
-        bool any_bad = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!(want >> i & 1u) || (ids[i] >= 0 && ids[i] < args.num_blocks)) continue;
-          want &= ~(1u << i);
-          any_bad = true;
-          const int k0 = (lane + 32 * i) * rows;  // the block's keys, a run inside a word or whole words
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            if (rows >= 32 ? (w >= k0 / 32 && w < (k0 + rows) / 32) : w == k0 / 32)
-              bad[w] |= rows >= 32 ? 0xffffffffu : ((1u << rows) - 1u) << (k0 & 31);
-        }
-        if (__any_sync(0xffffffffu, any_bad)) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) bad[w] = __reduce_or_sync(0xffffffffu, bad[w]);
-          if (lane == 0) atomicOr(&g_status, kStatusBadBlock);
-        }
-        const uint32_t bytes = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(want))) * rows * 256u;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int s = kvi % NS;
-          if (kvi >= NS) ok = mbar_wait_warp(smem_u32(&sm.kv_empty[s]), ((kvi / NS) - 1) & 1, abort_flag);
-          if (!ok) break;
-          const uint32_t bar = smem_u32(&sm.kv_full[s]);
-          if (lane == 0) {
-            // The tile four before is done with these words: the V tile filled last took the
-            // place of that of three tiles before this one, whose PV was complete.
-            if (v == 0)
-              for (int w = 0; w < 4; ++w) sm.bad[(kvi >> 1) & 3][w] = bad[w];
-            mbar_arrive_expect_tx(bar, bytes);
+      // Loads tile j; `id`: this lane's entry of the tile's first 32 blocks (the rest, of
+      // blocks of one or two keys, is looked up here).
+      auto load_tile = [&](const Piece& p, int j, int id) {
+        const int s = n % NS;
+        if (n >= NS) ok = mbar_wait_warp(smem_u32(&empty[s]), ((n / NS) - 1) & 1, abort_flag);
+        if (!ok) return;
+        const uint32_t bar = smem_u32(&full[s]);
+        // Tile n - 4 is done with these words: K's stage was that of tile n - 2, whose S
+        // followed the PV of tile n - 4 or a later one in the same slot.
+        if (is_k && lane < BN / 32) sm.bad[n & 3][lane] = 0u;
+        __syncwarp();
+        const int y = (j * BN) & ((1 << args.block_shift) - 1) & ~(rows - 1);
+#pragma unroll 1
+        for (int b0 = 0; b0 < nblk; b0 += 32) {
+          const int blk = b0 + lane;
+          if (b0 > 0) id = lookup(p, j, blk);
+          const bool want = wanted(p, j, blk), good = want && id >= 0 && id < args.num_blocks;
+          if (__any_sync(0xffffffffu, want && !good)) {
+            if (want && !good) {  // a run of keys inside a word, or whole words
+              const uint32_t run = rows >= 32 ? 0xffffffffu : ((1u << rows) - 1u) << (blk * rows & 31);
+              for (int w = blk * rows / 32; is_k && w < max(1, rows / 32) + blk * rows / 32; ++w) atomicOr(&sm.bad[n & 3][w], run);
+              atomicOr(&g_status, kStatusBadBlock);
+            }
           }
+          unsigned live = __ballot_sync(0xffffffffu, good);
+          if (lane == 0) mbar_expect_tx(bar, __popc(live) * rows * 256u);
           __syncwarp();
-          const CUtensorMap* tm = v ? &tm_v : &tm_k;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (want >> i & 1u) {
-              const uint32_t dst = smem_u32(sm.kv[s]) + (lane + 32 * i) * rows * 128;
-              const int z = ids[i] * geo.Hkv + p.kvh;
+          for (; live; live &= live - 1) {
+            const int src = __ffs(live) - 1;
+            const int z = __shfl_sync(0xffffffffu, id, src) * geo.Hkv + p.kvh;
+            const uint32_t dst = ring + s * TILE_BYTES + (b0 + src) * rows * 128;
+            if (elect_one()) {
               tma_load_3d(dst, tm, bar, 0, y, z);
               tma_load_3d(dst + HALF_BYTES, tm, bar, 64, y, z);
             }
-          __syncwarp();
-          ++kvi;
+          }
         }
-        p = pn;
-        j = jn;
-        more = more_n;
-        want = want_next;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ids[i] = ids_next[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+        ++n;
+      };
+      // The first piece from i on that has keys; -1: none is left.
+      auto find = [&](int i) {
+        while (pieces.wait(i)) {
+          if (pieces.at(i).j0 < pieces.at(i).j1) return i;
+          pieces.release(i++, lane);
+        }
+        return -1;
+      };
+      int ip = find(0), j = 0, even = 0, odd = 0;
+      if (ip >= 0) {
+        j = pieces.at(ip).j0;
+        even = lookup(pieces.at(ip), j, lane);
       }
-      for (int i = max(0, kvi - NS); i < kvi; ++i) mbar_wait_drain(smem_u32(&sm.kv_full[i % NS]), (i / NS) & 1);
+      // One tile: the next one's entries are asked for, then this one is loaded.
+      auto step = [&](int cur, int& next) {
+        int in = ip, jn = j + 1;
+        if (jn == pieces.at(ip).j1) {
+          in = find(ip + 1);
+          if (in >= 0) jn = pieces.at(in).j0;
+        }
+        if (in >= 0) next = lookup(pieces.at(in), jn, lane);
+        if (is_k && j == pieces.at(ip).j0) load_q(pieces.at(ip));
+        if (ok) load_tile(pieces.at(ip), j, cur);
+        if (in != ip) pieces.release(ip, lane);
+        ip = in;
+        j = jn;
+      };
+      while (ok && ip >= 0) {
+        step(even, odd);
+        if (ok && ip >= 0) step(odd, even);
+      }
+      for (int i = max(0, n - NS); i < n; ++i) mbar_wait_drain(smem_u32(&full[i % NS]), (i / NS) & 1);
+      if (nq0 > 0) mbar_wait_drain(smem_u32(&sm.q_full[0]), (nq0 - 1) & 1);
+      if (nq1 > 0) mbar_wait_drain(smem_u32(&sm.q_full[1]), (nq1 - 1) & 1);
     } else {
       // ---------------------------------------------------------- MMA issuer
       // The whole warp runs this (warp-uniform waits); MMAs and commits go out from one
       // elected lane.
-      int base = 0;           // key tiles of the pieces before this one (ring position / 2)
+      int base = 0;  // key tiles of the pieces before this one
+      int np = 0;    // items started
       // Phase bits, bit t for slot t: Q_PH q_full, P_PH p_full and O_PH o_free to wait for
       // next; O_USED: an item has used O_t; Q_HERE: the item's Q tile has landed.
       enum : uint32_t { Q_PH = 0, P_PH = 2, O_PH = 4, O_USED = 6, Q_HERE = 8 };
       uint32_t ph = 0;
       auto bit = [&](uint32_t i) { return (ph >> i) & 1u; };
       bool ok = true;
-      Piece p;
-      while (ok && pieces.next(p, lane)) {
-        const int nt = p.j1 - p.j0;
-        if (nt == 0) continue;
+      for (int ip = 0; ok && pieces.wait(ip); ++ip) {
+        const Piece& p = pieces.at(ip);
+        const int j0 = p.j0, j1 = p.j1;
+        if (j0 == j1) {
+          pieces.release(ip, lane);
+          continue;
+        }
         ph &= ~(3u << Q_HERE);
-        const int k0 = 2 * (base - p.j0);  // ring entries of tile j: K k0 + 2 j, V the next
-        auto addr = [&](int i) { return smem_u32(sm.kv[i % NS]); };
-        auto wait_kv = [&](int i) {
-          return mbar_wait_warp(smem_u32(&sm.kv_full[i % NS]), static_cast<uint32_t>((i / NS) & 1), abort_flag);
+        const int n0 = base - j0;  // tile j is the rings' entry n0 + j
+        auto k_addr = [&](int j) { return smem_u32(sm.k[(n0 + j) % NS]); };
+        auto v_addr = [&](int j) { return smem_u32(sm.v[(n0 + j) % NS]); };
+        auto wait_k = [&](int j) {
+          return mbar_wait_warp(smem_u32(&sm.k_full[(n0 + j) % NS]), static_cast<uint32_t>(((n0 + j) / NS) & 1), abort_flag);
         };
-        auto free_kv = [&](int i) { commit_elect(smem_u32(&sm.kv_empty[i % NS])); };
+        auto wait_v = [&](int j) {
+          return mbar_wait_warp(smem_u32(&sm.v_full[(n0 + j) % NS]), static_cast<uint32_t>(((n0 + j) / NS) & 1), abort_flag);
+        };
+        auto free_k = [&](int j) { commit_elect(smem_u32(&sm.k_empty[(n0 + j) % NS])); };
+        auto free_v = [&](int j) { commit_elect(smem_u32(&sm.v_empty[(n0 + j) % NS])); };
         // S_t of key tile j from Q slot qs; `last`: the item's last use of that slot.
         auto issue_s = [&](int t, int qs, int j, bool last) {
           if (!bit(Q_HERE + qs)) {
@@ -603,7 +623,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ph ^= 1u << (Q_PH + qs);
             ph |= 1u << (Q_HERE + qs);
           }
-          issue_qk<T>(tmem + 128 * t, smem_u32(sm.q[qs]), addr(k0 + 2 * j));
+          issue_qk<T>(tmem + 128 * t, smem_u32(sm.q[qs]), k_addr(j));
           commit_elect(smem_u32(&sm.s_full[t]));
           if (last) commit_elect(smem_u32(&sm.q_empty[qs]));
           return true;
@@ -618,7 +638,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!mbar_wait_warp(smem_u32(&sm.p_full[t]), bit(P_PH + t), abort_flag)) return false;
           ph ^= 1u << (P_PH + t);
           tc_fence_after();
-          issue_pv<T>(tmem + 256 + 128 * t, tmem + 128 * t, addr(k0 + 2 * j + 1), first ? 0u : 1u);
+          issue_pv<T>(tmem + 256 + 128 * t, tmem + 128 * t, v_addr(j), first ? 0u : 1u);
           if (last) {
             commit_elect(smem_u32(&sm.o_full[t]));
             ph |= 1u << (O_USED + t);
@@ -627,51 +647,55 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         };
         // V_j has landed; its rows without a key of the item are cleared.
         auto ready_v = [&](int j) {
-          if (!wait_kv(k0 + 2 * j + 1)) return false;
-          const uint32_t* bad = sm.bad[(k0 / 2 + j) & 3];
-          const int lo = p.key_lo - j * BN, hi = p.key_hi - j * BN;
-          if (lo > 0 || hi < BN || (bad[0] | bad[1] | bad[2] | bad[3]) != 0u)
-            zero_v_rows(addr(k0 + 2 * j + 1), lo, hi, bad, lane);
+          if (!wait_v(j)) return false;
+          const uint4 bad = *reinterpret_cast<const uint4*>(sm.bad[(n0 + j) & 3]);
+          if (j == j0 || j == j1 - 1 || (bad.x | bad.y | bad.z | bad.w) != 0u) {
+            const int lo = p.key_lo - j * BN, hi = p.key_hi - j * BN;
+            if (lo > 0 || hi < BN || (bad.x | bad.y | bad.z | bad.w) != 0u)
+              zero_v_rows(v_addr(j), lo, hi, sm.bad[(n0 + j) & 3], lane);
+          }
           return true;
         };
         if (one_tile(geo, p)) {
           // Slots take turns: S of tile j + 2 follows PV of tile j in the same slot.
-          for (int j = p.j0; ok && j < min(p.j1, p.j0 + 2); ++j) {
-            ok = wait_kv(k0 + 2 * j) && issue_s(j - p.j0, 0, j, j == p.j1 - 1);
-            if (ok) free_kv(k0 + 2 * j);
+          for (int j = j0; ok && j < min(j1, j0 + 2); ++j) {
+            ok = wait_k(j) && issue_s(j - j0, np & 1, j, j == j1 - 1);
+            if (ok) free_k(j);
           }
-          for (int j = p.j0; ok && j < p.j1; ++j) {
-            const int t = (j - p.j0) & 1;
-            const bool next = j + 2 < p.j1;
-            ok = ready_v(j) && (!next || wait_kv(k0 + 2 * j + 4)) && issue_o(t, j, j < p.j0 + 2, !next);
+          for (int j = j0; ok && j < j1; ++j) {
+            const int t = (j - j0) & 1;
+            const bool next = j + 2 < j1;
+            ok = ready_v(j) && (!next || wait_k(j + 2)) && issue_o(t, j, j < j0 + 2, !next);
             if (!ok) break;
-            free_kv(k0 + 2 * j + 1);
+            free_v(j);
             if (next) {
-              ok = issue_s(t, 0, j + 2, j + 2 == p.j1 - 1);
-              if (ok) free_kv(k0 + 2 * j + 4);
+              ok = issue_s(t, np & 1, j + 2, j + 2 == j1 - 1);
+              if (ok) free_k(j + 2);
             }
           }
         } else {
           const Tiles t0 = slot_tiles(geo, p, 0), t1 = slot_tiles(geo, p, 1);
-          ok = wait_kv(k0 + 2 * p.j0);
-          if (ok && t0.has(p.j0)) ok = issue_s(0, 0, p.j0, p.j0 == t0.end - 1);
-          if (ok && t1.has(p.j0)) ok = issue_s(1, 1, p.j0, p.j0 == t1.end - 1);
-          if (ok) free_kv(k0 + 2 * p.j0);
-          for (int j = p.j0; ok && j < p.j1; ++j) {
-            const bool next = j + 1 < p.j1;
-            ok = ready_v(j) && (!next || wait_kv(k0 + 2 * j + 2));
+          ok = wait_k(j0);
+          if (ok && t0.has(j0)) ok = issue_s(0, 0, j0, j0 == t0.end - 1);
+          if (ok && t1.has(j0)) ok = issue_s(1, 1, j0, j0 == t1.end - 1);
+          if (ok) free_k(j0);
+          for (int j = j0; ok && j < j1; ++j) {
+            const bool next = j + 1 < j1;
+            ok = ready_v(j) && (!next || wait_k(j + 1));
             if (ok && t0.has(j)) ok = issue_o(0, j, j == t0.first, j == t0.end - 1);
             if (ok && next && t0.has(j + 1)) ok = issue_s(0, 0, j + 1, j + 1 == t0.end - 1);
             if (ok && t1.has(j)) ok = issue_o(1, j, j == t1.first, j == t1.end - 1);
             if (!ok) break;
-            free_kv(k0 + 2 * j + 1);
+            free_v(j);
             if (next) {
               if (t1.has(j + 1)) ok = issue_s(1, 1, j + 1, j + 1 == t1.end - 1);
-              if (ok) free_kv(k0 + 2 * j + 2);
+              if (ok) free_k(j + 1);
             }
           }
         }
-        base += nt;
+        base += j1 - j0;
+        ++np;
+        pieces.release(ip, lane);
       }
       // All MMAs issued by this warp must complete before TMEM is freed.
       commit_elect(smem_u32(&sm.mma_done));
@@ -691,8 +715,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t stage = smem_u32(sm.stage[wq]);
     int nfull[2] = {0, 0};
     bool ok = true;
-    Piece p;
-    while (ok && pieces.next(p, lane)) {
+    for (int ip = 0; ok && pieces.wait(ip); pieces.release(ip++, lane)) {
+      const Piece& p = pieces.at(ip);
       const bool single = one_tile(geo, p);
       for (int t = 0; t < (single ? 1 : 2) && ok; ++t) {
         const int nrows = tile_rows(geo, p, t);
@@ -837,19 +861,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int nst = 0;   // items published
     int base = 0;  // key tiles of the pieces before this one
     bool ok = true;
-    Piece p;
-    while (ok && pieces.next(p, lane)) {
+    for (int ip = 0; ok && pieces.wait(ip); ++ip) {
+      const Piece p = pieces.at(ip);
+      pieces.release(ip, lane);
       const Tiles my = slot_tiles(geo, p, t);
       const int tbase = base - p.j0;
       base += p.j1 - p.j0;
       if (!my.any()) continue;
-      const bool single = one_tile(geo, p);
-      const int rt = single ? 0 : t;  // the slot's row tile
-      const int nrows = tile_rows(geo, p, rt);
-      const bool busy = wq * 32 < nrows;
-      const int p_first = p.pos0 + rt * geo.tpt;                           // positions of the tile's first
-      const int p_last = p_first + min(p.ntok - rt * geo.tpt, geo.tpt) - 1;  // and last token
-      const int row_p = p_first + row_tok;
+      const int rt = one_tile(geo, p) ? 0 : t;  // the slot's row tile
+      const bool busy = wq * 32 < tile_rows(geo, p, rt);
+      // Keys that this row sees, [row_lo, row_hi), and that every row of the tile sees,
+      // [all_lo, all_hi): key tiles inside the latter need no mask.
+      int row_lo = p.key_lo, row_hi = p.key_hi, all_lo = p.key_lo, all_hi = p.key_hi;
+      {
+        const int first = p.pos0 + rt * geo.tpt, last = first + min(p.ntok - rt * geo.tpt, geo.tpt) - 1;
+        if (geo.causal) {
+          row_hi = min(row_hi, first + row_tok + 1);
+          all_hi = min(all_hi, first + 1);
+        }
+        if (geo.window > 0) {
+          row_lo = max(row_lo, first + row_tok - geo.window + 1);
+          all_lo = max(all_lo, last - geo.window + 1);
+        }
+      }
       float m = -INFINITY, l = 0.f;
       bool nan_row = false;
       for (int j = my.first; j < my.end; j += my.step, ++ns) {
@@ -863,13 +897,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int kb = j * BN;
         const uint4 bad = *reinterpret_cast<const uint4*>(sm.bad[(tbase + j) & 3]);
         const bool any_bad = (bad.x | bad.y | bad.z | bad.w) != 0u;
-        if (kb + BN > p.key_hi || kb < p.key_lo || (geo.causal && kb + BN - 1 > p_first) ||
-            (geo.window > 0 && kb <= p_last - geo.window) || any_bad) {
+        if (kb + BN > all_hi || kb < all_lo || any_bad) {
           // Visible keys of this row: columns [c_lo, c_hi), without the blocks outside the pool.
-          int c_hi = min(BN, p.key_hi - kb), c_lo = max(0, p.key_lo - kb);
-          if (geo.causal) c_hi = min(c_hi, row_p - kb + 1);
-          if (geo.window > 0) c_lo = max(c_lo, row_p - geo.window + 1 - kb);
-          c_hi = max(c_hi, c_lo);
+          const int c_lo = max(0, row_lo - kb), c_hi = max(min(BN, row_hi - kb), c_lo);
 #pragma unroll 1
           for (int c = 0; c < BN / 32; ++c) {
             const uint32_t bw = c == 0 ? bad.x : c == 1 ? bad.y : c == 2 ? bad.z : bad.w;
