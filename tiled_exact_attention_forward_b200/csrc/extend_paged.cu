@@ -75,11 +75,22 @@ struct Piece {
   int pad;
 };
 
-struct Smem {
-  uint8_t q[2][TILE_BYTES];
-  uint8_t k[NS][TILE_BYTES];
-  uint8_t v[NS][TILE_BYTES];
-  uint8_t stage[4][HALF_BYTES / 4];  // epilogue, per warp: 32 rows of 128 bytes
+// Dynamic shared memory, 1024-byte aligned: Q tiles, K ring, V ring, then the epilogue's
+// staging, 32 rows of 128 bytes per warp.
+constexpr int kKOff = 2 * TILE_BYTES;
+constexpr int kVOff = kKOff + NS * TILE_BYTES;
+constexpr int kStageOff = kVOff + NS * TILE_BYTES;
+constexpr int kStageBytes = 32 * 128;
+constexpr size_t kSmemBytes = kStageOff + 4 * kStageBytes + 1024;
+
+// Heads per key head and tokens per row tile, 128 / G.
+struct Geo {
+  int G, tpt;
+};
+
+// Everything else sits in static shared memory, whose addresses are constants: pointers
+// to it cost no registers.
+struct Ctl {
   uint32_t bad[4][BN / 32];          // keys of a tile whose block lies outside the pool
   Piece piece[NP];
   uint64_t piece_full[NP], piece_empty[NP];
@@ -96,57 +107,51 @@ struct Smem {
   long long start_unit;              // units before the sequence the run starts in
   long long start_units;             // its units per key head
   int start_b;                       // that sequence
+  Geo geo;
   uint32_t tmem_base;
   int abort_flag;
 };
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-
-// Sizes and mask of a launch, in registers.
-struct Geo {
-  int T, B, Hq, Hkv, G, tpt;  // tpt: tokens per row tile, 128 / G
-  int causal, window, cap;
-};
+static_assert(kSmemBytes + sizeof(Ctl) + 64 <= 227 * 1024, "shared memory");
 
 struct Seq {
   int tok0, nq, n;  // first packed token, new tokens, keys
 };
-__device__ __forceinline__ Seq seq_of(const ExtendArgs& a, const Geo& g, int b) {
+__device__ __forceinline__ Seq seq_of(const ExtendArgs& a, int b) {
   Seq s;
   if (a.cu_tokens == nullptr) {
     s.tok0 = b;
     s.nq = 1;
   } else {
-    s.tok0 = min(max(a.cu_tokens[b], 0), g.T);
-    s.nq = min(max(a.cu_tokens[b + 1], s.tok0), g.T) - s.tok0;
+    s.tok0 = min(max(a.cu_tokens[b], 0), a.T);
+    s.nq = min(max(a.cu_tokens[b + 1], s.tok0), a.T) - s.tok0;
   }
-  s.n = min(max(a.seqlens[b], 0), g.cap);
+  s.n = min(max(a.seqlens[b], 0), a.cap);
   return s;
 }
 
 // Keys [lo, hi) that tokens at positions pf .. pl of a sequence with n keys see in all
 // (empty: lo = hi = 0).
-__device__ __forceinline__ void key_range(const Geo& g, int pf, int pl, int n, int& lo, int& hi) {
-  hi = g.causal ? min(n, pl + 1) : n;
-  lo = g.window > 0 ? max(0, pf - g.window + 1) : 0;
+__device__ __forceinline__ void key_range(const ExtendArgs& a, int pf, int pl, int n, int& lo, int& hi) {
+  hi = a.causal ? min(n, pl + 1) : n;
+  lo = a.window > 0 ? max(0, pf - a.window + 1) : 0;
   if (hi <= lo) lo = hi = 0;
 }
 // Key tiles of item p (tokens [2 tpt p, 2 tpt (p + 1)) of the sequence).
-__device__ __forceinline__ int item_tiles(const Geo& g, const Seq& s, int p, int& lo, int& hi) {
+__device__ __forceinline__ int item_tiles(const ExtendArgs& a, const Geo& g, const Seq& s, int p, int& lo, int& hi) {
   const int i0 = p * 2 * g.tpt, i1 = min(s.nq, i0 + 2 * g.tpt);
-  key_range(g, s.n - s.nq + i0, s.n - s.nq + i1 - 1, s.n, lo, hi);
+  key_range(a, s.n - s.nq + i0, s.n - s.nq + i1 - 1, s.n, lo, hi);
   return hi > lo ? (hi + BN - 1) / BN - lo / BN : 0;
 }
 __device__ __forceinline__ int items_of(const Geo& g, int nq) { return (nq + 2 * g.tpt - 1) / (2 * g.tpt); }
 
 // Units of all items of one key head of each lane's sequence (lane: its own `s`, nq = 0
 // for none).  Sequences with many items are summed by the whole warp.
-__device__ __forceinline__ long long head_units(const Geo& g, const Seq& s, int lane) {
+__device__ __forceinline__ long long head_units(const ExtendArgs& a, const Geo& g, const Seq& s, int lane) {
   const int np = items_of(g, s.nq);
   long long u = 0;
   int lo, hi;
   if (np <= 4)
-    for (int p = 0; p < np; ++p) u += 1 + item_tiles(g, s, p, lo, hi);
+    for (int p = 0; p < np; ++p) u += 1 + item_tiles(a, g, s, p, lo, hi);
   unsigned many = __ballot_sync(0xffffffffu, np > 4);
   while (many) {
     const int src = __ffs(many) - 1;
@@ -155,7 +160,7 @@ __device__ __forceinline__ long long head_units(const Geo& g, const Seq& s, int 
                 __shfl_sync(0xffffffffu, s.n, src)};
     const int onp = items_of(g, o.nq);
     long long v = 0;
-    for (int p = lane; p < onp; p += 32) v += 1 + item_tiles(g, o, p, lo, hi);
+    for (int p = lane; p < onp; p += 32) v += 1 + item_tiles(a, g, o, p, lo, hi);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
     if (lane == src) u = v;
@@ -163,19 +168,21 @@ __device__ __forceinline__ long long head_units(const Geo& g, const Seq& s, int 
   return u;
 }
 
-// The key tiles of piece p that slot t works on: first, end (exclusive) and step.
+// The key tiles of piece p that slot t works on: first, end (exclusive) and step; `base`:
+// key tiles of the CTA's pieces before p.  One-tile items' tiles take the slots in turn,
+// through the items: the CTA's tile number g goes to slot g % 2.
 struct Tiles {
   int first, end, step;
   __device__ __forceinline__ bool any() const { return first < end; }
   __device__ __forceinline__ bool has(int j) const { return j >= first && j < end; }  // two-tile items only
 };
 __device__ __forceinline__ bool one_tile(const Geo& g, const Piece& p) { return p.ntok <= g.tpt; }
-__device__ __forceinline__ Tiles slot_tiles(const Geo& g, const Piece& p, int t) {
-  if (one_tile(g, p)) return Tiles{p.j0 + t, p.j1, 2};
+__device__ __forceinline__ Tiles slot_tiles(const ExtendArgs& a, const Geo& g, const Piece& p, int t, int base) {
+  if (one_tile(g, p)) return Tiles{p.j0 + ((t ^ base) & 1), p.j1, 2};
   const int i0 = t * g.tpt, i1 = min(p.ntok, i0 + g.tpt);
   int lo = p.key_lo, hi = p.key_hi;
-  if (g.causal) hi = min(hi, p.pos0 + i1);
-  if (g.window > 0) lo = max(lo, p.pos0 + i0 - g.window + 1);
+  if (a.causal) hi = min(hi, p.pos0 + i1);
+  if (a.window > 0) lo = max(lo, p.pos0 + i0 - a.window + 1);
   if (hi <= lo) return Tiles{p.j0, p.j0, 1};
   return Tiles{max(p.j0, lo / BN), min(p.j1, (hi + BN - 1) / BN), 1};
 }
@@ -215,14 +222,11 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
   mma8_ts<idesc, col_step, v_step>(d_tmem, p_tmem, desc_lo(v_addr, HALF_BYTES), desc_hi(1024), accumulate);
 }
 
-#define FA_TMEM_LD16(taddr, r)                                                                       \
-  asm volatile(                                                                                      \
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"   \
-      "%15}, [%16];"                                                                                 \
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),          \
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),      \
-        "=r"(r[14]), "=r"(r[15])                                                                     \
-      : "r"(taddr))
+#define FA_TMEM_LD8(taddr, r)                                                                        \
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"              \
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), \
+                 "=r"(r[7])                                                                          \
+               : "r"(taddr))
 
 // A warp's view of the planner's ring of pieces.  Pieces stay in shared memory until the
 // warp releases them: what a role needs of one now and then is read there, since a
@@ -230,7 +234,7 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
 // L1 is left to catch it (measured: 60 bytes of spills in the MMA and producer warps
 // took a quarter of the kernel's time).
 struct Pieces {
-  Smem* sm;
+  Ctl* sm;
   volatile int* abort_flag;
   __device__ __forceinline__ const Piece& at(int i) const { return sm->piece[i % NP]; }
   // Waits for piece i; false at the end (or when the CTA gives up).
@@ -261,15 +265,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ExtendArgs args, int q_box_tokens) {
   extern __shared__ uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ Ctl sm;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int wg = warp >> 2;
-  Geo geo;
-  geo.T = args.T; geo.B = args.B; geo.Hq = args.Hq; geo.Hkv = args.Hkv;
-  geo.G = args.Hq / args.Hkv;
-  geo.tpt = BM / geo.G;
-  geo.causal = args.causal; geo.window = args.window; geo.cap = args.cap;
+  const Geo geo0{args.Hq / args.Hkv, BM / (args.Hq / args.Hkv)};
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     mbar_init(smem_u32(&sm.mma_done), 1);
     sm.abort_flag = 0;
+    sm.geo = geo0;
     fence_barrier_init();
   }
   if (warp == MMA_WARP) {
@@ -311,12 +312,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // are held one to a thread; more are walked in chunks, twice.
   long long total = 0, mine = 0;
   long long mine_units = 0;
-  for (int c = 0; c < geo.B; c += NUM_THREADS) {
+  for (int c = 0; c < args.B; c += NUM_THREADS) {
     Seq s{0, 0, 0};
-    if (c + static_cast<int>(threadIdx.x) < geo.B) s = seq_of(args, geo, c + threadIdx.x);
-    const long long u = head_units(geo, s, lane);
+    if (c + static_cast<int>(threadIdx.x) < args.B) s = seq_of(args, c + threadIdx.x);
+    const long long u = head_units(args, geo0, s, lane);
     mine_units = u;
-    mine = u * geo.Hkv;
+    mine = u * args.Hkv;
     total += mine;
   }
 #pragma unroll
@@ -331,13 +332,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const long long u_begin = blockIdx.x * run, u_end = min(total, u_begin + run);
   if (u_begin < u_end) {
     long long before = 0;  // units of the chunks already walked
-    for (int c = 0; c < geo.B; c += NUM_THREADS) {
-      if (geo.B > NUM_THREADS) {
+    for (int c = 0; c < args.B; c += NUM_THREADS) {
+      if (args.B > NUM_THREADS) {
         Seq s{0, 0, 0};
-        if (c + static_cast<int>(threadIdx.x) < geo.B) s = seq_of(args, geo, c + threadIdx.x);
-        const long long u = head_units(geo, s, lane);
+        if (c + static_cast<int>(threadIdx.x) < args.B) s = seq_of(args, c + threadIdx.x);
+        const long long u = head_units(args, geo0, s, lane);
         mine_units = u;
-        mine = u * geo.Hkv;
+        mine = u * args.Hkv;
       }
       long long inc = mine;  // inclusive scan over the block
 #pragma unroll
@@ -367,15 +368,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
   const Pieces pieces{&sm, abort_flag};
+  // Each role reads these for itself: a value held across the roles is one register less
+  // for the role that has none to spare.
+  auto tiles_base = [&]() { return (smem_u32(smem_raw) + 1023u) & ~1023u; };
+  auto geometry = [&]() { return Geo{*const_cast<volatile int*>(&sm.geo.G), *const_cast<volatile int*>(&sm.geo.tpt)}; };
+  auto tmem_base = [&]() { return *const_cast<volatile uint32_t*>(&sm.tmem_base); };
 
   if (wg == 3) {
     regs_dec<kOtherRegs>();
     if (warp == PLAN_WARP) {
       // ---------------------------------------------------------- planner
       // Walks the run item by item and hands out its pieces.
+      const Geo geo = geometry();
       ExtendDesc open{0, 0, 0, -1};  // the item that begins here and ends in another CTA
       int ip = 0;                    // pieces handed out
       auto hand_out = [&](const Piece& p) {
@@ -392,14 +398,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool ok = true;
       if (u_begin < u_end && sm.start_b >= 0) {
         int b = sm.start_b;
-        Seq s = seq_of(args, geo, b);
+        Seq s = seq_of(args, b);
         const long long into = u_begin - sm.start_unit;
         int h = static_cast<int>(into / sm.start_units);
         // The item of key head h in which the run starts, 32 items at a time.
         long long rem = into % sm.start_units;
         int p = 0, lo, hi;
         for (const int np = items_of(geo, s.nq); p < np; p += 32) {
-          int inc = p + lane < np ? 1 + item_tiles(geo, s, p + lane, lo, hi) : 0;
+          int inc = p + lane < np ? 1 + item_tiles(args, geo, s, p + lane, lo, hi) : 0;
           const int own = inc;
 #pragma unroll
           for (int x = 1; x < 32; x <<= 1) {
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         long long u0 = u_begin - rem;  // the item's first unit
         while (ok && u0 < u_end) {
-          const int nt = item_tiles(geo, s, p, lo, hi);
+          const int nt = item_tiles(args, geo, s, p, lo, hi);
           // Tile k of the item is unit u0 + 1 + k; the item's own unit u0 only says who
           // writes an item without keys.
           const int k0 = static_cast<int>(max(0LL, u_begin - u0 - 1)), k1 = static_cast<int>(min(static_cast<long long>(nt), u_end - u0 - 1));
@@ -442,13 +448,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           u0 += 1 + nt;
           if (++p >= items_of(geo, s.nq)) {
             p = 0;
-            if (++h >= geo.Hkv) {
+            if (++h >= args.Hkv) {
               h = 0;
               do {
-                if (++b >= geo.B) break;
-                s = seq_of(args, geo, b);
+                if (++b >= args.B) break;
+                s = seq_of(args, b);
               } while (s.nq == 0);
-              if (b >= geo.B) break;
+              if (b >= args.B) break;
             }
           }
         }
@@ -464,11 +470,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // A warp each, so that K tiles run ahead of the V tiles that wait for a softmax.
       // Lane l holds the tile's block-table entries l, l + 32, ..., fetched one tile ahead
       // (across items too); the boxes go out one after another from one elected lane.
+      const Geo geo = geometry();
+      const uint32_t tiles = tiles_base();
       const bool is_k = warp == K_WARP;
       const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
       uint64_t* full = is_k ? sm.k_full : sm.v_full;
       uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
-      const uint32_t ring = is_k ? smem_u32(sm.k[0]) : smem_u32(sm.v[0]);
+      const uint32_t ring = tiles + (is_k ? kKOff : kVOff);
       const int rows = min(1 << args.block_shift, BN);  // keys per box
       const int nblk = BN / rows;                       // blocks per tile: 1 .. 128
       // Does block `blk` of tile j hold keys of the item?
@@ -488,7 +496,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto load_q = [&](const Piece& p) {
         const bool single = one_tile(geo, p);
         for (int t = 0; t < (single ? 1 : 2); ++t) {
-          if (!single && !slot_tiles(geo, p, t).any()) continue;
+          if (!single && !slot_tiles(args, geo, p, t, 0).any()) continue;
           const int qs = single ? np & 1 : t;
           const int used = qs ? nq1++ : nq0++;
           if (used > 0) ok = ok && mbar_wait_warp(smem_u32(&sm.q_empty[qs]), (used - 1) & 1, abort_flag);
@@ -500,7 +508,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int box_rows = q_box_tokens * geo.G;
             mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * box_rows * 256));
             for (int i = 0; i < boxes; ++i) {
-              const uint32_t dst = smem_u32(sm.q[qs]) + i * box_rows * 128;
+              const uint32_t dst = tiles + qs * TILE_BYTES + i * box_rows * 128;
               const int tok = p.tok0 + t * geo.tpt + i * q_box_tokens;
               tma_load_3d(dst, &tm_q, bar, 0, p.kvh * geo.G, tok);
               tma_load_3d(dst + HALF_BYTES, &tm_q, bar, 64, p.kvh * geo.G, tok);
@@ -539,7 +547,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           __syncwarp();
           for (; live; live &= live - 1) {
             const int src = __ffs(live) - 1;
-            const int z = __shfl_sync(0xffffffffu, id, src) * geo.Hkv + p.kvh;
+            const int z = __shfl_sync(0xffffffffu, id, src) * args.Hkv + p.kvh;
             const uint32_t dst = ring + s * TILE_BYTES + (b0 + src) * rows * 128;
             if (elect_one()) {
               tma_load_3d(dst, tm, bar, 0, y, z);
@@ -588,114 +596,125 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else {
       // ---------------------------------------------------------- MMA issuer
       // The whole warp runs this (warp-uniform waits); MMAs and commits go out from one
-      // elected lane.
-      int base = 0;  // key tiles of the pieces before this one
-      int np = 0;    // items started
-      // Phase bits, bit t for slot t: Q_PH q_full, P_PH p_full and O_PH o_free to wait for
-      // next; O_USED: an item has used O_t; Q_HERE: the item's Q tile has landed.
-      enum : uint32_t { Q_PH = 0, P_PH = 2, O_PH = 4, O_USED = 6, Q_HERE = 8 };
+      // elected lane.  Phase bits, bit t for slot t: Q_PH q_full, P_PH p_full and O_PH
+      // o_free to wait for next; O_USED: an item has used O_t.
+      const Geo geo = geometry();
+      const uint32_t tiles = tiles_base(), tmem = tmem_base();
+      enum : uint32_t { Q_PH = 0, P_PH = 2, O_PH = 4, O_USED = 6 };
       uint32_t ph = 0;
       auto bit = [&](uint32_t i) { return (ph >> i) & 1u; };
       bool ok = true;
-      for (int ip = 0; ok && pieces.wait(ip); ++ip) {
-        const Piece& p = pieces.at(ip);
-        const int j0 = p.j0, j1 = p.j1;
-        if (j0 == j1) {
-          pieces.release(ip, lane);
-          continue;
+      // g: a key tile's number in the CTA, its place in both rings.
+      auto wait_k = [&](int g) {
+        return mbar_wait_warp(smem_u32(&sm.k_full[g % NS]), static_cast<uint32_t>((g / NS) & 1), abort_flag);
+      };
+      auto free_k = [&](int g) { commit_elect(smem_u32(&sm.k_empty[g % NS])); };
+      auto free_v = [&](int g) { commit_elect(smem_u32(&sm.v_empty[g % NS])); };
+      // S_t of tile g from Q slot qs; `first`, `last`: the item's uses of that Q slot.
+      auto issue_s = [&](int t, int qs, int g, bool first, bool last) {
+        if (first) {
+          if (!mbar_wait_warp(smem_u32(&sm.q_full[qs]), bit(Q_PH + qs), abort_flag)) return false;
+          ph ^= 1u << (Q_PH + qs);
         }
-        ph &= ~(3u << Q_HERE);
-        const int n0 = base - j0;  // tile j is the rings' entry n0 + j
-        auto k_addr = [&](int j) { return smem_u32(sm.k[(n0 + j) % NS]); };
-        auto v_addr = [&](int j) { return smem_u32(sm.v[(n0 + j) % NS]); };
-        auto wait_k = [&](int j) {
-          return mbar_wait_warp(smem_u32(&sm.k_full[(n0 + j) % NS]), static_cast<uint32_t>(((n0 + j) / NS) & 1), abort_flag);
-        };
-        auto wait_v = [&](int j) {
-          return mbar_wait_warp(smem_u32(&sm.v_full[(n0 + j) % NS]), static_cast<uint32_t>(((n0 + j) / NS) & 1), abort_flag);
-        };
-        auto free_k = [&](int j) { commit_elect(smem_u32(&sm.k_empty[(n0 + j) % NS])); };
-        auto free_v = [&](int j) { commit_elect(smem_u32(&sm.v_empty[(n0 + j) % NS])); };
-        // S_t of key tile j from Q slot qs; `last`: the item's last use of that slot.
-        auto issue_s = [&](int t, int qs, int j, bool last) {
-          if (!bit(Q_HERE + qs)) {
-            if (!mbar_wait_warp(smem_u32(&sm.q_full[qs]), bit(Q_PH + qs), abort_flag)) return false;
-            ph ^= 1u << (Q_PH + qs);
-            ph |= 1u << (Q_HERE + qs);
+        issue_qk<T>(tmem + 128 * t, tiles + qs * TILE_BYTES, tiles + kKOff + g % NS * TILE_BYTES);
+        commit_elect(smem_u32(&sm.s_full[t]));
+        if (last) commit_elect(smem_u32(&sm.q_empty[qs]));
+        return true;
+      };
+      // PV_t of tile g, once P is there.  The slot's first of an item overwrites O_t (which
+      // the epilogue must have read out), its last publishes it.
+      auto issue_o = [&](int t, int g, bool first, bool last) {
+        if (first && bit(O_USED + t)) {
+          if (!mbar_wait_warp(smem_u32(&sm.o_free[t]), bit(O_PH + t), abort_flag)) return false;
+          ph ^= 1u << (O_PH + t);
+        }
+        if (!mbar_wait_warp(smem_u32(&sm.p_full[t]), bit(P_PH + t), abort_flag)) return false;
+        ph ^= 1u << (P_PH + t);
+        tc_fence_after();
+        issue_pv<T>(tmem + 256 + 128 * t, tmem + 128 * t, tiles + kVOff + g % NS * TILE_BYTES, first ? 0u : 1u);
+        if (last) {
+          commit_elect(smem_u32(&sm.o_full[t]));
+          ph |= 1u << (O_USED + t);
+        }
+        return true;
+      };
+      // V of tile j of piece p (number g) has landed; its rows without a key of the item are cleared.
+      auto ready_v = [&](const Piece& p, int j, int g) {
+        if (!mbar_wait_warp(smem_u32(&sm.v_full[g % NS]), static_cast<uint32_t>((g / NS) & 1), abort_flag)) return false;
+        const uint4 bad = *reinterpret_cast<const uint4*>(sm.bad[g & 3]);
+        const int lo = p.key_lo - j * BN, hi = p.key_hi - j * BN;
+        if (lo > 0 || hi < BN || (bad.x | bad.y | bad.z | bad.w) != 0u)
+          zero_v_rows(tiles + kVOff + g % NS * TILE_BYTES, lo, hi, sm.bad[g & 3], lane);
+        return true;
+      };
+      // One-tile items: their key tiles form one stream through the items.  S runs up to two
+      // tiles ahead of PV, S of tile g + 2 following PV of tile g in its slot, so that the
+      // softmaxes of two tiles (of the same or of successive items) overlap.
+      int is = 0, sj = 0, gs = 0, np = 0;  // S's piece, its next tile, that one's number; items begun
+      bool s_open = false;
+      auto advance_s = [&]() {
+        while (!s_open) {
+          if (!pieces.wait(is)) return false;
+          const Piece& p = pieces.at(is);
+          if (p.j0 < p.j1) {
+            if (!one_tile(geo, p)) return false;  // two-tile items issue their own
+            s_open = true;
+            sj = p.j0;
+          } else {
+            ++is;
           }
-          issue_qk<T>(tmem + 128 * t, smem_u32(sm.q[qs]), k_addr(j));
-          commit_elect(smem_u32(&sm.s_full[t]));
-          if (last) commit_elect(smem_u32(&sm.q_empty[qs]));
-          return true;
-        };
-        // PV_t of key tile j, once P is there.  The slot's first overwrites O_t (which the
-        // epilogue must have read out), its last publishes it.
-        auto issue_o = [&](int t, int j, bool first, bool last) {
-          if (first && bit(O_USED + t)) {
-            if (!mbar_wait_warp(smem_u32(&sm.o_free[t]), bit(O_PH + t), abort_flag)) return false;
-            ph ^= 1u << (O_PH + t);
-          }
-          if (!mbar_wait_warp(smem_u32(&sm.p_full[t]), bit(P_PH + t), abort_flag)) return false;
-          ph ^= 1u << (P_PH + t);
-          tc_fence_after();
-          issue_pv<T>(tmem + 256 + 128 * t, tmem + 128 * t, v_addr(j), first ? 0u : 1u);
-          if (last) {
-            commit_elect(smem_u32(&sm.o_full[t]));
-            ph |= 1u << (O_USED + t);
-          }
-          return true;
-        };
-        // V_j has landed; its rows without a key of the item are cleared.
-        auto ready_v = [&](int j) {
-          if (!wait_v(j)) return false;
-          const uint4 bad = *reinterpret_cast<const uint4*>(sm.bad[(n0 + j) & 3]);
-          if (j == j0 || j == j1 - 1 || (bad.x | bad.y | bad.z | bad.w) != 0u) {
-            const int lo = p.key_lo - j * BN, hi = p.key_hi - j * BN;
-            if (lo > 0 || hi < BN || (bad.x | bad.y | bad.z | bad.w) != 0u)
-              zero_v_rows(v_addr(j), lo, hi, sm.bad[(n0 + j) & 3], lane);
-          }
-          return true;
-        };
+        }
+        const Piece& p = pieces.at(is);
+        const bool last = sj + 1 == p.j1;
+        ok = wait_k(gs) && issue_s(gs & 1, np & 1, gs, sj == p.j0, last);
+        if (!ok) return false;
+        free_k(gs);
+        ++gs;
+        ++sj;
+        if (last) {
+          s_open = false;
+          ++is;
+          ++np;
+        }
+        return true;
+      };
+      int g = 0;  // the number of the next tile to take its PV
+      for (int ip = 0; ok && pieces.wait(ip); pieces.release(ip++, lane)) {
+        const Piece& p = pieces.at(ip);
+        if (p.j0 == p.j1) continue;
         if (one_tile(geo, p)) {
-          // Slots take turns: S of tile j + 2 follows PV of tile j in the same slot.
-          for (int j = j0; ok && j < min(j1, j0 + 2); ++j) {
-            ok = wait_k(j) && issue_s(j - j0, np & 1, j, j == j1 - 1);
-            if (ok) free_k(j);
-          }
-          for (int j = j0; ok && j < j1; ++j) {
-            const int t = (j - j0) & 1;
-            const bool next = j + 2 < j1;
-            ok = ready_v(j) && (!next || wait_k(j + 2)) && issue_o(t, j, j < j0 + 2, !next);
-            if (!ok) break;
-            free_v(j);
-            if (next) {
-              ok = issue_s(t, np & 1, j + 2, j + 2 == j1 - 1);
-              if (ok) free_k(j + 2);
+          for (int j = p.j0; ok && j < p.j1; ++j, ++g) {
+            while (gs < g + 2 && advance_s()) {
             }
+            ok = ok && ready_v(p, j, g) && issue_o(g & 1, g, j < p.j0 + 2, j + 2 >= p.j1);
+            if (ok) free_v(g);
           }
         } else {
-          const Tiles t0 = slot_tiles(geo, p, 0), t1 = slot_tiles(geo, p, 1);
-          ok = wait_k(j0);
-          if (ok && t0.has(j0)) ok = issue_s(0, 0, j0, j0 == t0.end - 1);
-          if (ok && t1.has(j0)) ok = issue_s(1, 1, j0, j0 == t1.end - 1);
-          if (ok) free_k(j0);
-          for (int j = j0; ok && j < j1; ++j) {
+          // Two row tiles, a slot each: PV_0, next S_0, PV_1, next S_1.
+          const Tiles t0 = slot_tiles(args, geo, p, 0, 0), t1 = slot_tiles(args, geo, p, 1, 0);
+          const int j1 = p.j1;
+          int j = p.j0;
+          ok = wait_k(g);
+          if (ok && t0.has(j)) ok = issue_s(0, 0, g, true, j == t0.end - 1);
+          if (ok && t1.has(j)) ok = issue_s(1, 1, g, true, j == t1.end - 1);
+          if (ok) free_k(g);
+          for (; ok && j < j1; ++j, ++g) {
             const bool next = j + 1 < j1;
-            ok = ready_v(j) && (!next || wait_k(j + 1));
-            if (ok && t0.has(j)) ok = issue_o(0, j, j == t0.first, j == t0.end - 1);
-            if (ok && next && t0.has(j + 1)) ok = issue_s(0, 0, j + 1, j + 1 == t0.end - 1);
-            if (ok && t1.has(j)) ok = issue_o(1, j, j == t1.first, j == t1.end - 1);
+            ok = ready_v(p, j, g) && (!next || wait_k(g + 1));
+            if (ok && t0.has(j)) ok = issue_o(0, g, j == t0.first, j == t0.end - 1);
+            if (ok && next && t0.has(j + 1)) ok = issue_s(0, 0, g + 1, j + 1 == t0.first, j + 1 == t0.end - 1);
+            if (ok && t1.has(j)) ok = issue_o(1, g, j == t1.first, j == t1.end - 1);
             if (!ok) break;
-            free_v(j);
+            free_v(g);
             if (next) {
-              if (t1.has(j + 1)) ok = issue_s(1, 1, j + 1, j + 1 == t1.end - 1);
-              if (ok) free_k(j + 1);
+              if (t1.has(j + 1)) ok = issue_s(1, 1, g + 1, j + 1 == t1.first, j + 1 == t1.end - 1);
+              if (ok) free_k(g + 1);
             }
           }
+          is = ip + 1;
+          gs = g;
+          ++np;
         }
-        base += j1 - j0;
-        ++np;
-        pieces.release(ip, lane);
       }
       // All MMAs issued by this warp must complete before TMEM is freed.
       commit_elect(smem_u32(&sm.mma_done));
@@ -710,51 +729,54 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     regs_dec<kEpilogueRegs>();
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
-    const int row_tok = row / geo.G, row_head = row - row_tok * geo.G;
+    const Geo geo = geometry();
+    const uint32_t tmem = tmem_base();
+    const uint32_t stage = tiles_base() + kStageOff + wq * kStageBytes;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t stage = smem_u32(sm.stage[wq]);
-    int nfull[2] = {0, 0};
+    uint32_t ph = 0;  // phase of o_full (and st_full) to wait for next, bit t for slot t
+    int base = 0;     // key tiles of the pieces before this one
     bool ok = true;
     for (int ip = 0; ok && pieces.wait(ip); pieces.release(ip++, lane)) {
       const Piece& p = pieces.at(ip);
       const bool single = one_tile(geo, p);
-      for (int t = 0; t < (single ? 1 : 2) && ok; ++t) {
-        const int nrows = tile_rows(geo, p, t);
-        const bool valid = row < nrows;
-        const long long out_row =
-            static_cast<long long>(p.tok0 + t * geo.tpt + row_tok) * geo.Hq + p.kvh * geo.G + row_head;
-        const long long part_row = p.slot < 0 ? 0 : static_cast<long long>(p.slot) * args.slot_rows + t * BM + row;
-        const bool on = slot_tiles(geo, p, t).any();
-        const bool both = single && slot_tiles(geo, p, 1).any();
-        if (!on) {
+      const int slot = p.slot;
+      for (int rt = 0; rt < (single ? 1 : 2) && ok; ++rt) {
+        const int t = single ? base & 1 : rt;  // the slot; a one-tile item's first
+        const int nrows = tile_rows(geo, p, rt);
+        const bool both = single && p.j1 - p.j0 > 1;
+        // This row's place in the output or, for a piece, in the workspace.
+        long long at;
+        if (slot < 0) {
+          const int tok = row / geo.G;
+          at = static_cast<long long>(p.tok0 + rt * geo.tpt + tok) * args.Hq + p.kvh * geo.G + row - tok * geo.G;
+        } else {
+          at = static_cast<long long>(slot) * args.slot_rows + rt * BM + row;
+        }
+        float* lse = slot < 0 ? args.lse : args.ws_lse;
+        if (!slot_tiles(args, geo, p, t, base).any()) {
           // No key tile: a whole item's rows see nothing; a piece adds nothing.
-          if (valid) {
-            if (p.slot >= 0) {
-              args.ws_lse[part_row] = -INFINITY;
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.o) + out_row * D);
-#pragma unroll
+          if (row < nrows) {
+            if (lse != nullptr) lse[at] = -INFINITY;
+            if (slot < 0) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.o) + at * D);
+#pragma unroll 1
               for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-              if (args.lse != nullptr) args.lse[out_row] = -INFINITY;
             }
           }
           continue;
         }
-        ok = mbar_wait_warp(smem_u32(&sm.o_full[t]), nfull[t] & 1, abort_flag) &&
-             mbar_wait_warp(smem_u32(&sm.st_full[t]), nfull[t] & 1, abort_flag);
-        if (ok && both)
-          ok = mbar_wait_warp(smem_u32(&sm.o_full[1]), nfull[1] & 1, abort_flag) &&
-               mbar_wait_warp(smem_u32(&sm.st_full[1]), nfull[1] & 1, abort_flag);
+        for (int i = 0; ok && i < (both ? 2 : 1); ++i)
+          ok = mbar_wait_warp(smem_u32(&sm.o_full[t ^ i]), ph >> (t ^ i) & 1u, abort_flag) &&
+               mbar_wait_warp(smem_u32(&sm.st_full[t ^ i]), ph >> (t ^ i) & 1u, abort_flag);
         if (!ok) break;
-        ++nfull[t];
-        if (both) ++nfull[1];
+        ph ^= both ? 3u : 1u << t;
         tc_fence_after();
         float m = sm.stat_m[t][row], l = sm.stat_l[t][row];
         mbar_arrive(smem_u32(&sm.st_empty[t]));
         float f0 = 1.f, f1 = 0.f;
         if (both) {
-          const float m1 = sm.stat_m[1][row], l1 = sm.stat_l[1][row];
-          mbar_arrive(smem_u32(&sm.st_empty[1]));
+          const float m1 = sm.stat_m[t ^ 1][row], l1 = sm.stat_l[t ^ 1][row];
+          mbar_arrive(smem_u32(&sm.st_empty[t ^ 1]));
           const float mm = fmaxf(m, m1);
           f0 = m == -INFINITY ? 0.f : ex2_approx((m - mm) * args.scale_log2);
           f1 = m1 == -INFINITY ? 0.f : ex2_approx((m1 - mm) * args.scale_log2);
@@ -762,147 +784,149 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           m = mm;
         }
         // l > 0: the row saw keys; l = 0: none; NaN marks a NaN score.
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         const bool none = l == 0.f;
+        if (row < nrows && lse != nullptr) lse[at] = l > 0.f ? m * args.scale + logf(l) : (none ? -INFINITY : l);
+        const float inv = l > 0.f ? 1.f / l : (none ? 0.f : l);
         f0 *= inv;
         f1 *= inv;
         const uint32_t tO = tmem + lane_off + 256 + t * 128;
-        const bool part = p.slot >= 0;
-        // 16 columns per step; four steps (16-bit) or two (float32) fill 128 bytes a row.
-        const int steps = part ? 2 : 4;
+        const uint32_t tO1 = tmem + lane_off + 256 + (t ^ 1) * 128;
+        const bool part = slot >= 0;
+        char* out = part ? reinterpret_cast<char*>(args.ws_o) : static_cast<char*>(args.o);
+        at *= part ? D * 4 : D * 2;  // bytes from here on
+        // 8 columns per step; eight steps (16-bit) or four (float32) fill 128 bytes a row.
+        // A warp without a row to write only frees the slots.
+        const int steps = part ? 4 : 8;
 #pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t o[16];
-          FA_TMEM_LD16(tO + 16 * c, o);
+        for (int c = wq * 32 < nrows ? 0 : D / 8; c < D / 8; ++c) {
+          uint32_t o[8];
+          FA_TMEM_LD8(tO + 8 * c, o);
           if (both) {
-            uint32_t o1[16];
-            FA_TMEM_LD16(tO + 128 + 16 * c, o1);
+            uint32_t o1[8];
+            FA_TMEM_LD8(tO1 + 8 * c, o1);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 8; ++e)
               o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e]) * f0));
           } else {
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
-          }
-          if (c == D / 16 - 1) {
-            tc_fence_before();
-            mbar_arrive(smem_u32(&sm.o_free[t]));
-            if (both) mbar_arrive(smem_u32(&sm.o_free[1]));
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
           }
           if (none) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0u;
+            for (int e = 0; e < 8; ++e) o[e] = 0u;
           }
           const int step = c & (steps - 1);
           if (step == 0) __syncwarp();  // the stage's last rows have been read
+          // 16-byte chunk i of a row's 128 bytes sits at chunk i ^ (row % 8).
+          const uint32_t dst = stage + lane * 128, sw = (lane & 7) << 4;
           if (part) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const uint32_t dst = stage + lane * 128 + (((4 * step + v) ^ (lane & 7)) << 4);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(o[4 * v]), "r"(o[4 * v + 1]),
-                           "r"(o[4 * v + 2]), "r"(o[4 * v + 3])
+            for (int v = 0; v < 2; ++v)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((2 * step + v) << 4) ^ sw)), "r"(o[4 * v]),
+                           "r"(o[4 * v + 1]), "r"(o[4 * v + 2]), "r"(o[4 * v + 3])
                            : "memory");
-            }
           } else {
+            uint32_t w[4];
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const uint32_t dst = stage + lane * 128 + (((2 * step + v) ^ (lane & 7)) << 4);
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = pack2<T>(__uint_as_float(o[8 * v + 2 * i]), __uint_as_float(o[8 * v + 2 * i + 1]));
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                           : "memory");
-            }
+            for (int i = 0; i < 4; ++i) w[i] = pack2<T>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((step << 4) ^ sw)), "r"(w[0]), "r"(w[1]),
+                         "r"(w[2]), "r"(w[3])
+                         : "memory");
           }
           if (step == steps - 1) {
             __syncwarp();
             // Eight lanes a row, four rows a step.
-            char* out = part ? reinterpret_cast<char*>(args.ws_o) : static_cast<char*>(args.o);
-            const long long my_byte = part ? part_row * (D * 4) + (c / 2) * 128 : out_row * (D * 2) + (c / 4) * 128;
+            const int ch = (lane & 7) << 4;
 #pragma unroll 1
-            for (int r = 0; r < 32; r += 4) {
-              if (wq * 32 + r >= nrows) break;
-              const int rr = r + (lane >> 3), ch = lane & 7;
-              const long long at = __shfl_sync(0xffffffffu, my_byte, rr);
+            for (int r = lane >> 3; r - (lane >> 3) + wq * 32 < nrows && r < 32; r += 4) {
+              const long long row_at = __shfl_sync(0xffffffffu, at, r);
               uint4 v;
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                           : "r"(stage + rr * 128 + ((ch ^ (rr & 7)) << 4)));
-              if (wq * 32 + rr < nrows) *reinterpret_cast<uint4*>(out + at + ch * 16) = v;
+                           : "r"(stage + r * 128 + (ch ^ ((r & 7) << 4))));
+              if (wq * 32 + r < nrows) *reinterpret_cast<uint4*>(out + row_at + ch) = v;
             }
+            at += 128;
           }
         }
-        if (valid) {
-          const float lse = l > 0.f ? m * args.scale + logf(l) : (none ? -INFINITY : l);
-          if (part)
-            args.ws_lse[part_row] = lse;
-          else if (args.lse != nullptr)
-            args.lse[out_row] = lse;
-        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sm.o_free[t]));
+        if (both) mbar_arrive(smem_u32(&sm.o_free[t ^ 1]));
       }
+      base += p.j1 - p.j0;
     }
   } else {
     // ------------------------------------------------------------ softmax warps
     // Warpgroup t is the softmax of slot t: thread = row, all 128 score columns of a key
     // tile in registers (as in fwd_tc.cu).  A warp without a valid row only keeps step.
     regs_inc<kSoftmaxRegs>();
+    const Geo geo = geometry();
+    const uint32_t tmem = tmem_base();
     const int t = wg;
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
-    const int row_tok = row / geo.G;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off + t * 128;
-    const uint32_t tO = tmem + lane_off + 256 + t * 128;
+    const uint32_t tO = tS + 256;
     const float sl2 = args.scale_log2;
-    int ns = 0;    // S tiles consumed
-    int nst = 0;   // items published
+    // Phase bits: S_PH s_full to wait for next, ST_PH st_empty, ST_ANY an item was published.
+    enum : uint32_t { S_PH = 1, ST_PH = 2, ST_ANY = 4 };
+    uint32_t ph = ST_PH;
     int base = 0;  // key tiles of the pieces before this one
     bool ok = true;
     for (int ip = 0; ok && pieces.wait(ip); ++ip) {
-      const Piece p = pieces.at(ip);
-      pieces.release(ip, lane);
-      const Tiles my = slot_tiles(geo, p, t);
-      const int tbase = base - p.j0;
-      base += p.j1 - p.j0;
-      if (!my.any()) continue;
-      const int rt = one_tile(geo, p) ? 0 : t;  // the slot's row tile
-      const bool busy = wq * 32 < tile_rows(geo, p, rt);
       // Keys that this row sees, [row_lo, row_hi), and that every row of the tile sees,
       // [all_lo, all_hi): key tiles inside the latter need no mask.
-      int row_lo = p.key_lo, row_hi = p.key_hi, all_lo = p.key_lo, all_hi = p.key_hi;
+      int row_lo, row_hi, all_lo, all_hi;
+      int j, end, step, bad_at;  // bad_at + j: the key tile's number in the CTA
+      bool busy;
       {
+        const Piece& p = pieces.at(ip);
+        const Tiles my = slot_tiles(args, geo, p, t, base);
+        j = my.first;
+        end = my.end;
+        step = my.step;
+        bad_at = base - p.j0;
+        base += p.j1 - p.j0;
+        const int rt = one_tile(geo, p) ? 0 : t;  // the slot's row tile
+        busy = wq * 32 < tile_rows(geo, p, rt);
+        row_lo = all_lo = p.key_lo;
+        row_hi = all_hi = p.key_hi;
         const int first = p.pos0 + rt * geo.tpt, last = first + min(p.ntok - rt * geo.tpt, geo.tpt) - 1;
-        if (geo.causal) {
-          row_hi = min(row_hi, first + row_tok + 1);
+        const int mine = first + row / geo.G;
+        if (args.causal) {
+          row_hi = min(row_hi, mine + 1);
           all_hi = min(all_hi, first + 1);
         }
-        if (geo.window > 0) {
-          row_lo = max(row_lo, first + row_tok - geo.window + 1);
-          all_lo = max(all_lo, last - geo.window + 1);
+        if (args.window > 0) {
+          row_lo = max(row_lo, mine - args.window + 1);
+          all_lo = max(all_lo, last - args.window + 1);
         }
+        pieces.release(ip, lane);
       }
+      if (j >= end) continue;
       float m = -INFINITY, l = 0.f;
-      bool nan_row = false;
-      for (int j = my.first; j < my.end; j += my.step, ++ns) {
-        ok = mbar_wait_warp(smem_u32(&sm.s_full[t]), ns & 1, abort_flag);
+      bool nan_row = false, begun = false;
+      for (; j < end; j += step) {
+        ok = mbar_wait_warp(smem_u32(&sm.s_full[t]), ph & S_PH, abort_flag);
         if (!ok) break;
+        ph ^= S_PH;
         if (!busy) {
           mbar_arrive(smem_u32(&sm.p_full[t]));
           continue;
         }
         tc_fence_after();
         const int kb = j * BN;
-        const uint4 bad = *reinterpret_cast<const uint4*>(sm.bad[(tbase + j) & 3]);
+        const uint4 bad = *reinterpret_cast<const uint4*>(sm.bad[(bad_at + j) & 3]);
         const bool any_bad = (bad.x | bad.y | bad.z | bad.w) != 0u;
         if (kb + BN > all_hi || kb < all_lo || any_bad) {
           // Visible keys of this row: columns [c_lo, c_hi), without the blocks outside the pool.
           const int c_lo = max(0, row_lo - kb), c_hi = max(min(BN, row_hi - kb), c_lo);
 #pragma unroll 1
           for (int c = 0; c < BN / 32; ++c) {
-            const uint32_t bw = c == 0 ? bad.x : c == 1 ? bad.y : c == 2 ? bad.z : bad.w;
+            const uint32_t bw = sm.bad[(bad_at + j) & 3][c];
             if (bw == 0u && __all_sync(0xffffffffu, c_lo <= 32 * c && c_hi >= 32 * c + 32)) continue;
             uint32_t r[32];
             if (__all_sync(0xffffffffu, c_hi <= 32 * c || c_lo >= 32 * c + 32)) {
@@ -948,7 +972,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           m = m_new;
           l *= alpha;
         }
-        if (j > my.first && __any_sync(0xffffffffu, need)) {
+        if (begun && __any_sync(0xffffffffu, need)) {
           // O_t's last update is complete: S_t of this tile was issued after it.
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -960,6 +984,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             FA_TMEM_ST32(tO + 32 * c, r);
           }
         }
+        begun = true;
         const float ms = (m == -INFINITY) ? 0.f : m * sl2;
         const uint64_t sl2x2 = f2_pack(sl2, sl2), nms2 = f2_pack(-ms, -ms);
         uint64_t acc[4] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
@@ -996,12 +1021,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       if (!ok) break;
-      if (nst > 0) ok = mbar_wait_warp(smem_u32(&sm.st_empty[t]), (nst - 1) & 1, abort_flag);
+      if (ph & ST_ANY) ok = mbar_wait_warp(smem_u32(&sm.st_empty[t]), (ph & ST_PH) != 0u, abort_flag);
       if (!ok) break;
+      ph = (ph ^ ST_PH) | ST_ANY;
       sm.stat_m[t][row] = m;
       sm.stat_l[t][row] = nan_row ? __uint_as_float(0x7fc00000u) : l;
       mbar_arrive(smem_u32(&sm.st_full[t]));
-      ++nst;
     }
   }
 
@@ -1009,7 +1034,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   if (warp == MMA_WARP) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(sm.tmem_base, 512);
   }
 }
 
