@@ -51,8 +51,8 @@ constexpr int V_WARP = 14;                  // V tiles
 constexpr int PLAN_WARP = 15;
 constexpr int NP = 8;                       // pieces in flight between the planner and the other warps
 constexpr int kPieceReaders = 15;           // warps that read a piece: MMA, K, V, 8 softmax, 4 epilogue
-constexpr int kSoftmaxRegs = 192;
-constexpr int kEpilogueRegs = 64;
+constexpr int kSoftmaxRegs = 184;
+constexpr int kEpilogueRegs = 80;
 constexpr int kOtherRegs = 64;
 constexpr int kLaunchRegs = 128;            // 65536 / NUM_THREADS: what the split draws on
 static_assert(2 * WG_THREADS * kSoftmaxRegs + WG_THREADS * kEpilogueRegs + WG_THREADS * kOtherRegs <=
@@ -61,7 +61,12 @@ static_assert(2 * WG_THREADS * kSoftmaxRegs + WG_THREADS * kEpilogueRegs + WG_TH
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
 // A CTA takes at least this many units, so that few keys are not scattered over so
 // many CTAs that joining them costs more than it saves.
-constexpr int kMinUnits = 3;
+constexpr int kMinUnits = 6;
+constexpr int kItemUnits = 5;
+constexpr int kPairUnits = 1;
+// Epilogue: up to so many rows of a warp are written by their own lanes; more go through
+// shared memory, so that a store instruction does not touch 32 lines.
+constexpr int kDirectRows = 8;
 
 // A run of key tiles [j0, j1) of one item, as the planner hands it to the other warps.
 struct Piece {
@@ -142,6 +147,14 @@ __device__ __forceinline__ int item_tiles(const ExtendArgs& a, const Geo& g, con
   key_range(a, s.n - s.nq + i0, s.n - s.nq + i1 - 1, s.n, lo, hi);
   return hi > lo ? (hi + BN - 1) / BN - lo / BN : 0;
 }
+// Units of a key tile of item p, and of the whole item with nt key tiles.
+__device__ __forceinline__ int tile_units(const Geo& g, const Seq& s, int p) {
+  return s.nq - p * 2 * g.tpt > g.tpt ? kPairUnits : 1;
+}
+__device__ __forceinline__ int item_units(const ExtendArgs& a, const Geo& g, const Seq& s, int p) {
+  int lo, hi;
+  return kItemUnits + item_tiles(a, g, s, p, lo, hi) * tile_units(g, s, p);
+}
 __device__ __forceinline__ int items_of(const Geo& g, int nq) { return (nq + 2 * g.tpt - 1) / (2 * g.tpt); }
 
 // Units of all items of one key head of each lane's sequence (lane: its own `s`, nq = 0
@@ -149,9 +162,8 @@ __device__ __forceinline__ int items_of(const Geo& g, int nq) { return (nq + 2 *
 __device__ __forceinline__ long long head_units(const ExtendArgs& a, const Geo& g, const Seq& s, int lane) {
   const int np = items_of(g, s.nq);
   long long u = 0;
-  int lo, hi;
   if (np <= 4)
-    for (int p = 0; p < np; ++p) u += 1 + item_tiles(a, g, s, p, lo, hi);
+    for (int p = 0; p < np; ++p) u += item_units(a, g, s, p);
   unsigned many = __ballot_sync(0xffffffffu, np > 4);
   while (many) {
     const int src = __ffs(many) - 1;
@@ -160,7 +172,7 @@ __device__ __forceinline__ long long head_units(const ExtendArgs& a, const Geo& 
                 __shfl_sync(0xffffffffu, s.n, src)};
     const int onp = items_of(g, o.nq);
     long long v = 0;
-    for (int p = lane; p < onp; p += 32) v += 1 + item_tiles(a, g, o, p, lo, hi);
+    for (int p = lane; p < onp; p += 32) v += item_units(a, g, o, p);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
     if (lane == src) u = v;
@@ -222,11 +234,34 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
   mma8_ts<idesc, col_step, v_step>(d_tmem, p_tmem, desc_lo(v_addr, HALF_BYTES), desc_hi(1024), accumulate);
 }
 
-#define FA_TMEM_LD8(taddr, r)                                                                        \
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"              \
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), \
-                 "=r"(r[7])                                                                          \
-               : "r"(taddr))
+#define FA_TMEM_LD16(taddr, r)                                                                       \
+  asm volatile(                                                                                      \
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"   \
+      "%15}, [%16];"                                                                                 \
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),          \
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),      \
+        "=r"(r[14]), "=r"(r[15])                                                                     \
+      : "r"(taddr))
+
+// 16 columns of a row's O, scaled and (both) joined with the other slot's; zero for a row
+// without a key, whatever its O holds.
+__device__ __forceinline__ void load_o16(uint32_t tO, uint32_t tO1, bool both, bool none, float f0, float f1, float (&o)[16]) {
+  uint32_t r[16];
+  FA_TMEM_LD16(tO, r);
+  if (both) {
+    uint32_t r1[16];
+    FA_TMEM_LD16(tO1, r1);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(r1[e]), f1, __uint_as_float(r[e]) * f0);
+  } else {
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(r[e]) * f0;
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) o[e] = none ? 0.f : o[e];
+}
 
 // A warp's view of the planner's ring of pieces.  Pieces stay in shared memory until the
 // warp releases them: what a role needs of one now and then is read there, since a
@@ -405,7 +440,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         long long rem = into % sm.start_units;
         int p = 0, lo, hi;
         for (const int np = items_of(geo, s.nq); p < np; p += 32) {
-          int inc = p + lane < np ? 1 + item_tiles(args, geo, s, p + lane, lo, hi) : 0;
+          int inc = p + lane < np ? item_units(args, geo, s, p + lane) : 0;
           const int own = inc;
 #pragma unroll
           for (int x = 1; x < 32; x <<= 1) {
@@ -424,28 +459,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         long long u0 = u_begin - rem;  // the item's first unit
         while (ok && u0 < u_end) {
           const int nt = item_tiles(args, geo, s, p, lo, hi);
-          // Tile k of the item is unit u0 + 1 + k; the item's own unit u0 only says who
-          // writes an item without keys.
-          const int k0 = static_cast<int>(max(0LL, u_begin - u0 - 1)), k1 = static_cast<int>(min(static_cast<long long>(nt), u_end - u0 - 1));
+          // Tile k of the item begins at unit u0 + kItemUnits + k * w, and the run that holds
+          // this unit takes it; unit u0 only says who writes an item without keys.
+          const int w = tile_units(geo, s, p);
+          auto tile_at = [&](long long u) {
+            const long long k = (u - u0 - kItemUnits + w - 1) / w;
+            return static_cast<int>(min(max(k, 0LL), static_cast<long long>(nt)));
+          };
+          const int k0 = u_begin <= u0 + kItemUnits ? 0 : tile_at(u_begin), k1 = u_end <= u0 + kItemUnits ? 0 : tile_at(u_end);
           if (k0 < k1 || (nt == 0 && u0 >= u_begin)) {
-            Piece w;
+            Piece out;
             const int i0 = p * 2 * geo.tpt;
-            w.tok0 = s.tok0 + i0;
-            w.ntok = min(s.nq - i0, 2 * geo.tpt);
-            w.pos0 = s.n - s.nq + i0;
-            w.kvh = h;
-            w.b = b;
-            w.j0 = nt ? lo / BN + k0 : 0;
-            w.j1 = nt ? lo / BN + k1 : 0;
-            w.key_lo = lo;
-            w.key_hi = hi;
-            w.slot = k0 == 0 && k1 == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (k0 == 0 ? 1 : 0);
-            w.stop = 0;
-            w.pad = 0;
-            if (k0 == 0 && k1 < nt) open = ExtendDesc{w.tok0, w.ntok, h, static_cast<int>((u0 + nt) / run)};
-            ok = hand_out(w);
+            out.tok0 = s.tok0 + i0;
+            out.ntok = min(s.nq - i0, 2 * geo.tpt);
+            out.pos0 = s.n - s.nq + i0;
+            out.kvh = h;
+            out.b = b;
+            out.j0 = nt ? lo / BN + k0 : 0;
+            out.j1 = nt ? lo / BN + k1 : 0;
+            out.key_lo = lo;
+            out.key_hi = hi;
+            out.slot = k0 == 0 && k1 == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (k0 == 0 ? 1 : 0);
+            out.stop = 0;
+            out.pad = 0;
+            if (k0 == 0 && k1 < nt) open = ExtendDesc{out.tok0, out.ntok, h, static_cast<int>((u0 + kItemUnits + (nt - 1) * w) / run)};
+            ok = hand_out(out);
           }
-          u0 += 1 + nt;
+          u0 += kItemUnits + nt * w;
           if (++p >= items_of(geo, s.nq)) {
             p = 0;
             if (++h >= args.Hkv) {
@@ -724,8 +764,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (wg == EPI_WG) {
     // ------------------------------------------------------------ epilogue
     // Thread = one row of a tile.  O comes out of TMEM 16 columns at a time, is scaled
-    // (and, for a one-tile item, the two slots' states are joined), staged in the warp's
-    // own 4 KB and written in runs of 128 bytes a row: 16-bit O, or float32 partials.
+    // (and, for a one-tile item, the two slots' states are joined) and written: 16-bit O,
+    // or float32 partials.
     regs_dec<kEpilogueRegs>();
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
@@ -794,61 +834,67 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool part = slot >= 0;
         char* out = part ? reinterpret_cast<char*>(args.ws_o) : static_cast<char*>(args.o);
         at *= part ? D * 4 : D * 2;  // bytes from here on
-        // 8 columns per step; eight steps (16-bit) or four (float32) fill 128 bytes a row.
-        // A warp without a row to write only frees the slots.
-        const int steps = part ? 4 : 8;
+        const int mine = nrows - wq * 32;  // rows of this warp's 32 that hold a token
+        if (mine > 0 && mine <= kDirectRows) {
+          // A few rows: each lane writes its own.
+          char* dst = out + at;
 #pragma unroll 1
-        for (int c = wq * 32 < nrows ? 0 : D / 8; c < D / 8; ++c) {
-          uint32_t o[8];
-          FA_TMEM_LD8(tO + 8 * c, o);
-          if (both) {
-            uint32_t o1[8];
-            FA_TMEM_LD8(tO1 + 8 * c, o1);
-            tmem_ld_wait();
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            load_o16(tO + c, tO1 + c, both, none, f0, f1, o);
+            if (row < nrows) {
+              if (part) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e]) * f0));
-          } else {
-            tmem_ld_wait();
+                for (int v = 0; v < 4; ++v)
+                  *reinterpret_cast<float4*>(dst + c * 4 + v * 16) = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+              } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
-          }
-          if (none) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = 0u;
-          }
-          const int step = c & (steps - 1);
-          if (step == 0) __syncwarp();  // the stage's last rows have been read
-          // 16-byte chunk i of a row's 128 bytes sits at chunk i ^ (row % 8).
-          const uint32_t dst = stage + lane * 128, sw = (lane & 7) << 4;
-          if (part) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((2 * step + v) << 4) ^ sw)), "r"(o[4 * v]),
-                           "r"(o[4 * v + 1]), "r"(o[4 * v + 2]), "r"(o[4 * v + 3])
-                           : "memory");
-          } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = pack2<T>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((step << 4) ^ sw)), "r"(w[0]), "r"(w[1]),
-                         "r"(w[2]), "r"(w[3])
-                         : "memory");
-          }
-          if (step == steps - 1) {
-            __syncwarp();
-            // Eight lanes a row, four rows a step.
-            const int ch = (lane & 7) << 4;
-#pragma unroll 1
-            for (int r = lane >> 3; r - (lane >> 3) + wq * 32 < nrows && r < 32; r += 4) {
-              const long long row_at = __shfl_sync(0xffffffffu, at, r);
-              uint4 v;
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                           : "r"(stage + r * 128 + (ch ^ ((r & 7) << 4))));
-              if (wq * 32 + r < nrows) *reinterpret_cast<uint4*>(out + row_at + ch) = v;
+                for (int v = 0; v < 2; ++v)
+                  *reinterpret_cast<uint4*>(dst + c * 2 + v * 16) =
+                      make_uint4(pack2<T>(o[8 * v], o[8 * v + 1]), pack2<T>(o[8 * v + 2], o[8 * v + 3]),
+                                 pack2<T>(o[8 * v + 4], o[8 * v + 5]), pack2<T>(o[8 * v + 6], o[8 * v + 7]));
+              }
             }
-            at += 128;
+          }
+        } else if (mine > 0) {
+          // Staged: 64 16-bit or 32 float32 columns fill 128 bytes a row, which go out in runs,
+          // eight lanes a row.  16-byte chunk i of a row sits at chunk i ^ (row % 8).
+          const uint32_t dst = stage + lane * 128, sw = (lane & 7) << 4;
+          const int cols = part ? 32 : 64;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            load_o16(tO + c, tO1 + c, both, none, f0, f1, o);
+            const int in = c & (cols - 1);
+            if (in == 0) __syncwarp();  // the stage's last rows have been read
+            if (part) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((in * 4 + v * 16) ^ sw)),
+                             "f"(o[4 * v]), "f"(o[4 * v + 1]), "f"(o[4 * v + 2]), "f"(o[4 * v + 3])
+                             : "memory");
+            } else {
+#pragma unroll
+              for (int v = 0; v < 2; ++v)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((in * 2 + v * 16) ^ sw)),
+                             "r"(pack2<T>(o[8 * v], o[8 * v + 1])), "r"(pack2<T>(o[8 * v + 2], o[8 * v + 3])),
+                             "r"(pack2<T>(o[8 * v + 4], o[8 * v + 5])), "r"(pack2<T>(o[8 * v + 6], o[8 * v + 7]))
+                             : "memory");
+            }
+            if (in == cols - 16) {
+              __syncwarp();
+              const int ch = (lane & 7) << 4;
+#pragma unroll 2
+              for (int r = lane >> 3; r < 32; r += 4) {
+                const long long row_at = __shfl_sync(0xffffffffu, at, r);
+                uint4 v;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                             : "r"(stage + r * 128 + (ch ^ ((r & 7) << 4))));
+                if (r < mine) *reinterpret_cast<uint4*>(out + row_at + ch) = v;
+              }
+              at += 128;
+            }
           }
         }
         tc_fence_before();
