@@ -27,8 +27,9 @@
 //
 // Cache.  K and V tiles come by TMA, one box per block and 64-column half; blocks
 // with no visible key are not read.  Rows of a V tile outside the item's keys (a
-// block's unused tail, a skipped block) are zeroed in shared memory before the MMA:
-// their weights are zero, but 0 * NaN is not.
+// block's unused tail, a skipped block) stay out of the product: steps of 16 keys
+// without a key are not issued, other such rows are zeroed in shared memory before
+// the MMA, since their weights are zero but 0 * NaN is not.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -45,10 +46,10 @@ constexpr int NUM_THREADS = 512;
 constexpr int WARPS = NUM_THREADS / 32;
 constexpr int WG_THREADS = 128;
 constexpr int EPI_WG = 2;
-constexpr int MMA_WARP = 12;
-constexpr int K_WARP = 13;                  // Q and K tiles
-constexpr int V_WARP = 14;                  // V tiles
-constexpr int PLAN_WARP = 15;
+constexpr int PLAN_WARP = 12;
+constexpr int MMA_WARP = 13;
+constexpr int K_WARP = 14;                  // Q and K tiles
+constexpr int V_WARP = 15;                  // V tiles
 constexpr int NP = 8;                       // pieces in flight between the planner and the other warps
 constexpr int kPieceReaders = 15;           // warps that read a piece: MMA, K, V, 8 softmax, 4 epilogue
 constexpr int kSoftmaxRegs = 184;
@@ -243,6 +244,20 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
         "=r"(r[14]), "=r"(r[15])                                                                     \
       : "r"(taddr))
 
+// One step of 16 keys of O += P V.
+template <class T>
+__device__ __forceinline__ void issue_pv_step(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_addr, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 bd;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 bd, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(p_tmem), "r"(desc_lo(v_addr, HALF_BYTES)), "r"(desc_hi(1024)), "r"(accumulate),
+      "n"(idesc_f32acc<T>(BM, D, 0, 1))
+      : "memory");
+}
+
 // 16 columns of a row's O, scaled and (both) joined with the other slot's; zero for a row
 // without a key, whatever its O holds.
 __device__ __forceinline__ void load_o16(uint32_t tO, uint32_t tO1, bool both, bool none, float f0, float f1, float (&o)[16]) {
@@ -282,17 +297,17 @@ struct Pieces {
   }
 };
 
-// Zeroes the rows of a V tile that hold no key of the item: rows outside [lo, hi) and
-// rows of blocks outside the pool.  All lanes; ends with the writes visible to the MMA.
-__device__ __forceinline__ void zero_v_rows(uint32_t v_addr, int lo, int hi, const uint32_t* bad, int lane) {
+// Zeroes rows [r0, r1) of a V tile.  All lanes: sixteen to a row.
+__device__ __forceinline__ void zero_v_rows(uint32_t v_addr, int r0, int r1, int lane) {
   const uint32_t dst = v_addr + (lane >> 3 & 1) * HALF_BYTES + (lane & 7) * 16;
 #pragma unroll 1
-  for (int r = lane >> 4; r < BN; r += 2) {
-    if (r >= lo && r < hi && !((bad[r >> 5] >> (r & 31)) & 1u)) continue;
+  for (int r = r0 + (lane >> 4); r < r1; r += 2)
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + r * 128), "r"(0u) : "memory");
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
+}
+// Zeroes the rows of blocks outside the pool (bit r of `bad`).
+__device__ __noinline__ void zero_bad_rows(uint32_t v_addr, const uint32_t* bad, int lane) {
+  for (int r = 0; r < BN; ++r)
+    if (bad[r >> 5] >> (r & 31) & 1u) zero_v_rows(v_addr, r, r + 1, lane);
 }
 
 template <class T>
@@ -663,7 +678,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       };
       // PV_t of tile g, once P is there.  The slot's first of an item overwrites O_t (which
       // the epilogue must have read out), its last publishes it.
-      auto issue_o = [&](int t, int g, bool first, bool last) {
+      auto issue_o = [&](int t, int g, int2 steps, bool first, bool last) {
         if (first && bit(O_USED + t)) {
           if (!mbar_wait_warp(smem_u32(&sm.o_free[t]), bit(O_PH + t), abort_flag)) return false;
           ph ^= 1u << (O_PH + t);
@@ -671,20 +686,37 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!mbar_wait_warp(smem_u32(&sm.p_full[t]), bit(P_PH + t), abort_flag)) return false;
         ph ^= 1u << (P_PH + t);
         tc_fence_after();
-        issue_pv<T>(tmem + 256 + 128 * t, tmem + 128 * t, tiles + kVOff + g % NS * TILE_BYTES, first ? 0u : 1u);
+        const uint32_t v = tiles + kVOff + g % NS * TILE_BYTES;
+        if (steps.x == 0 && steps.y == BN / 16) {
+          issue_pv<T>(tmem + 256 + 128 * t, tmem + 128 * t, v, first ? 0u : 1u);
+        } else {
+#pragma unroll 1
+          for (int i = steps.x; i < steps.y; ++i)
+            issue_pv_step<T>(tmem + 256 + 128 * t, tmem + 128 * t + 8 * i, v + i * 16 * 128, first && i == steps.x ? 0u : 1u);
+        }
         if (last) {
           commit_elect(smem_u32(&sm.o_full[t]));
           ph |= 1u << (O_USED + t);
         }
         return true;
       };
-      // V of tile j of piece p (number g) has landed; its rows without a key of the item are cleared.
-      auto ready_v = [&](const Piece& p, int j, int g) {
+      // V of tile j of piece p (number g) has landed.  Rows without a key of the item are kept
+      // out of the product: whole steps of 16 keys are not issued (`steps`: first and end),
+      // the others' rows, and those of blocks outside the pool, are cleared.
+      auto ready_v = [&](const Piece& p, int j, int g, int2& steps) {
         if (!mbar_wait_warp(smem_u32(&sm.v_full[g % NS]), static_cast<uint32_t>((g / NS) & 1), abort_flag)) return false;
         const uint4 bad = *reinterpret_cast<const uint4*>(sm.bad[g & 3]);
-        const int lo = p.key_lo - j * BN, hi = p.key_hi - j * BN;
-        if (lo > 0 || hi < BN || (bad.x | bad.y | bad.z | bad.w) != 0u)
-          zero_v_rows(tiles + kVOff + g % NS * TILE_BYTES, lo, hi, sm.bad[g & 3], lane);
+        const int lo = max(0, p.key_lo - j * BN), hi = min(BN, p.key_hi - j * BN);
+        steps = make_int2(lo >> 4, (hi + 15) >> 4);
+        const bool any_bad = (bad.x | bad.y | bad.z | bad.w) != 0u;
+        if ((lo & 15) != 0 || (hi & 15) != 0 || any_bad) {
+          const uint32_t v = tiles + kVOff + g % NS * TILE_BYTES;
+          zero_v_rows(v, lo & ~15, lo, lane);
+          zero_v_rows(v, hi, (hi + 15) & ~15, lane);
+          if (any_bad) zero_bad_rows(v, sm.bad[g & 3], lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
         return true;
       };
       // One-tile items: their key tiles form one stream through the items.  S runs up to two
@@ -726,7 +758,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int j = p.j0; ok && j < p.j1; ++j, ++g) {
             while (gs < g + 2 && advance_s()) {
             }
-            ok = ok && ready_v(p, j, g) && issue_o(g & 1, g, j < p.j0 + 2, j + 2 >= p.j1);
+            int2 steps;
+            ok = ok && ready_v(p, j, g, steps) && issue_o(g & 1, g, steps, j < p.j0 + 2, j + 2 >= p.j1);
             if (ok) free_v(g);
           }
         } else {
@@ -740,10 +773,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (ok) free_k(g);
           for (; ok && j < j1; ++j, ++g) {
             const bool next = j + 1 < j1;
-            ok = ready_v(p, j, g) && (!next || wait_k(g + 1));
-            if (ok && t0.has(j)) ok = issue_o(0, g, j == t0.first, j == t0.end - 1);
+            int2 steps;
+            ok = ready_v(p, j, g, steps) && (!next || wait_k(g + 1));
+            if (ok && t0.has(j)) ok = issue_o(0, g, steps, j == t0.first, j == t0.end - 1);
             if (ok && next && t0.has(j + 1)) ok = issue_s(0, 0, g + 1, j + 1 == t0.first, j + 1 == t0.end - 1);
-            if (ok && t1.has(j)) ok = issue_o(1, g, j == t1.first, j == t1.end - 1);
+            if (ok && t1.has(j)) ok = issue_o(1, g, steps, j == t1.first, j == t1.end - 1);
             if (!ok) break;
             free_v(g);
             if (next) {
