@@ -144,7 +144,7 @@ class TestBindingChecks:
 
     @pytest.fixture(autouse=True)
     def meta(self, monkeypatch):
-        monkeypatch.setattr(fa, "_need_on", lambda device, **t: None)
+        monkeypatch.setattr(fa, "_on", lambda *t: 0)
         monkeypatch.setattr(fa, "_lib", lambda: pytest.fail("the C ABI was reached"))
 
     @staticmethod

@@ -31,6 +31,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -469,29 +470,39 @@ def attention(q, k, v, causal: bool = False, window: int = 0, scale=None):
     return _Attention.apply(q, k, v, bool(causal), int(window), scale)
 
 
-class _On:
-    """Makes a tensor's device the current one for a launch (nothing to do when it is)."""
-
-    def __init__(self, device):
-        self.to = device.index
-
-    def __enter__(self):
-        self.was = torch.cuda.current_device()
-        if self.was != self.to:
-            torch.cuda.set_device(self.to)
-
-    def __exit__(self, *exc):
-        if self.was != self.to:
-            torch.cuda.set_device(self.was)
+# The calls below are made once or more per layer and token, so their host time counts:
+# checks are plain comparisons, pointers and strides go to the C ABI as integers and
+# packed bytes (about 25 microseconds a call became 12).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_pack12 = struct.Struct("12q").pack
+_pack18 = struct.Struct("18q").pack
 
 
-def _need_on(device, **tensors):
-    """Each given tensor sits on `device`, a CUDA one (None entries are skipped)."""
-    if device.type != "cuda":
+def _on(first, *others):
+    """The CUDA device index of `first`; every other given tensor must sit there (None: skipped)."""
+    i = first.get_device()
+    if i < 0:
         raise ValueError("tensors must be on a CUDA device (there is no CPU path)")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, as the first tensor is")
+    for t in others:
+        if t is not None and t.get_device() != i:
+            raise ValueError("tensors must all be on the same CUDA device")
+    return i
+
+
+def _launch(fn, name, device, *args):
+    """fn(*args, stream) with `device` current and its current stream; raises on a non-FA_OK status."""
+    if _current_device() == device:
+        st = fn(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _raw_stream(device))
+    if st != FA_OK:
+        raise FAError(st, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _need_int32(name, t, shape):
@@ -499,21 +510,31 @@ def _need_int32(name, t, shape):
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
 
 
-def _heads_view(t, what):
-    """Sizes (B, H, N, d) and (batch, head, row) strides of a [B, H, N, d] or packed [T, H, d] tensor."""
-    if t.dim() == 4:
-        B, H, N, d = t.shape
-        st = t.stride()
-        strides = st[:3]
-    elif t.dim() == 3:
-        N, H, d = t.shape
-        st = t.stride()
-        B, strides = 1, (0, st[1], st[0])
-    else:
-        raise ValueError(f"{what} must be [B, H, N, d] or packed [T, H, d]")
+def _strides(t, packed):
+    """(batch, head, row) strides of a [B, H, N, d] or packed [T, H, d] tensor with contiguous rows."""
+    st = t.stride()
     if st[-1] != 1:
-        raise ValueError(f"{what}: the rows (last dimension) must be contiguous")
-    return (B, H, N, d), strides
+        raise ValueError("the rows (last dimension) of q, k, their outputs and gradients must be contiguous")
+    return (0, st[1], st[0]) if packed else st[:3]
+
+
+def _qk_sizes(q, k):
+    """(B, Hq, Hk, N, d, packed) of queries and keys, [B, H, N, d] or packed [T, H, d]."""
+    shape = q.shape
+    packed = len(shape) == 3
+    if packed:
+        N, Hq, d = shape
+        B = 1
+    elif len(shape) == 4:
+        B, Hq, N, d = shape
+    else:
+        raise ValueError("q must be [B, H, N, d] or packed [T, H, d]")
+    if k is None:
+        return B, Hq, 0, N, d, packed
+    Hk = k.shape[1]
+    if k.shape != ((N, Hk, d) if packed else (B, Hk, N, d)) or k.dtype != q.dtype:
+        raise ValueError("q and k must share dtype and every size but the heads")
+    return B, Hq, Hk, N, d, packed
 
 
 def _grad_like(t):
@@ -522,7 +543,7 @@ def _grad_like(t):
     return g if g.stride(-1) == 1 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _rotation_args(q, q_weight, k_weight, rope, eps, d):
+def _rotation_args(dtype, q_weight, k_weight, rope, eps, d):
     """(rot, max_pos, eps for the C ABI, weight dtype code) of a norm and rotation."""
     rot = max_pos = 0
     if rope is not None:
@@ -531,28 +552,42 @@ def _rotation_args(q, q_weight, k_weight, rope, eps, d):
         max_pos, rot = rope.shape
         if rot == 0 or rot % 16 or rot > d:
             raise ValueError("rope's second dimension must be a multiple of 16 up to the head dimension")
+    if eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("weights need eps: without it there is no norm")
+        return rot, max_pos, -1.0, _dtype_code(dtype)
+    if not eps >= 0:
+        raise ValueError("eps must be >= 0 (None: no norm)")
     wdt = None
     for w in (q_weight, k_weight):
         if w is None:
             continue
-        if eps is None:
-            raise ValueError("weights need eps: without it there is no norm")
         if w.shape != (d,) or not w.is_contiguous():
             raise ValueError("weights must be contiguous tensors of the head dimension")
-        if w.dtype not in (q.dtype, torch.float32) or (wdt is not None and w.dtype != wdt):
+        if w.dtype != (wdt or w.dtype) or (w.dtype != dtype and w.dtype != torch.float32):
             raise ValueError("weights must share one dtype: the tensors' or float32")
         wdt = w.dtype
-    if eps is not None and not eps >= 0:
-        raise ValueError("eps must be >= 0 (None: no norm)")
-    return rot, max_pos, -1.0 if eps is None else float(eps), _dtype_code(wdt if wdt is not None else q.dtype)
+    return rot, max_pos, float(eps), _dtype_code(wdt or dtype)
 
 
-def _positions_args(positions, B, N):
+def _position_stride(positions, B, N):
     if positions is None:
         return 0
     if positions.dtype != torch.int32 or positions.shape not in ((N,), (B, N)) or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int32 tensor [N] or [B, N] (packed: [T])")
     return N if positions.dim() == 2 else 0
+
+
+def _out_like(x, out):
+    """An output of x's sizes: the given one, checked, or a new contiguous one."""
+    if out is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("an output must have its input's shape and dtype")
+    return out
+
+
+_NO_STRIDES = (0, 0, 0)
 
 
 def norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6,
@@ -574,34 +609,21 @@ def norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=None
     calls take them; without k, q_out alone.  q_out, k_out may be given (at any
     strides, the inputs themselves among them).
     """
-    (B, Hq, N, d), qs = _heads_view(q, "q")
-    _need_on(q.device, k=k, q_weight=q_weight, k_weight=k_weight, rope=rope, positions=positions, q_out=q_out, k_out=k_out)
-    Hk, ks, kos = 0, (0, 0, 0), (0, 0, 0)
-    if k is not None:
-        kshape, ks = _heads_view(k, "k")
-        Hk = kshape[1]
-        if kshape != (B, Hk, N, d) or k.dim() != q.dim() or k.dtype != q.dtype:
-            raise ValueError("q and k must share dtype and every size but the heads")
-    elif k_weight is not None or k_out is not None:
+    device = _on(q, k, q_weight, k_weight, rope, positions, q_out, k_out)
+    B, Hq, Hk, N, d, packed = _qk_sizes(q, k)
+    if k is None and (k_weight is not None or k_out is not None):
         raise ValueError("k_weight and k_out need k")
-    rot, max_pos, e, wcode = _rotation_args(q, q_weight, k_weight, rope, eps, d)
-    pos_stride = _positions_args(positions, B, N)
-    for x, out in ((q, q_out), (k, k_out)):
-        if out is not None and (out.shape != x.shape or out.dtype != x.dtype):
-            raise ValueError("an output must have its input's shape and dtype")
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    qos = _heads_view(q_out, "q_out")[1]
+    rot, max_pos, e, wcode = _rotation_args(q.dtype, q_weight, k_weight, rope, eps, d)
+    pos_stride = _position_stride(positions, B, N)
+    q_out = _out_like(q, q_out)
+    ks = kos = _NO_STRIDES
     if k is not None:
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        kos = _heads_view(k_out, "k_out")[1]
-    with _On(q.device):
-        st = _lib().fa_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out),
-                                 (ctypes.c_longlong * 12)(*qs, *ks, *qos, *kos), _ptr(q_weight), _ptr(k_weight),
-                                 _ptr(rope), _ptr(positions), pos_stride, B, Hq, Hk, N, d, rot, max_pos, e,
-                                 int(bool(interleaved)), _dtype_code(q.dtype), wcode, _stream(q.device))
-    _check(st, "fa_norm_rope")
+        k_out = _out_like(k, k_out)
+        ks, kos = _strides(k, packed), _strides(k_out, packed)
+    strides = _pack12(*_strides(q, packed), *ks, *_strides(q_out, packed), *kos)
+    _launch(_lib().fa_norm_rope, "fa_norm_rope", device, q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out),
+            strides, _addr(q_weight), _addr(k_weight), _addr(rope), _addr(positions), pos_stride, B, Hq, Hk, N, d, rot, max_pos, e, int(bool(interleaved)),
+            _dtype_code(q.dtype), wcode)
     return (q_out, k_out) if k is not None else q_out
 
 
@@ -619,44 +641,35 @@ def norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope=
     A weight that is None has no gradient (None); weight gradients are summed in
     float32 in a fixed order and come in the weights' dtype.
     """
-    (B, Hq, N, d), qs = _heads_view(q, "q")
-    _need_on(q.device, k=k, dq_out=dq_out, dk_out=dk_out, q_weight=q_weight, k_weight=k_weight, rope=rope,
-             positions=positions, workspace=workspace)
+    device = _on(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, workspace)
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out go together")
-    Hk, ks, kgs, dks = 0, (0, 0, 0), (0, 0, 0), (0, 0, 0)
+    B, Hq, Hk, N, d, packed = _qk_sizes(q, k)
     if dq_out.shape != q.shape or dq_out.dtype != q.dtype:
         raise ValueError("dq_out must have q's shape and dtype")
-    qgs = _heads_view(dq_out, "dq_out")[1]
     dq, dk = _grad_like(q), None
+    ks = kgs = dks = _NO_STRIDES
     if k is not None:
-        kshape, ks = _heads_view(k, "k")
-        Hk = kshape[1]
-        if kshape != (B, Hk, N, d) or k.dim() != q.dim() or k.dtype != q.dtype:
-            raise ValueError("q and k must share dtype and every size but the heads")
         if dk_out.shape != k.shape or dk_out.dtype != k.dtype:
             raise ValueError("dk_out must have k's shape and dtype")
-        kgs = _heads_view(dk_out, "dk_out")[1]
         dk = _grad_like(k)
-        dks = _heads_view(dk, "dk")[1]
+        ks, kgs, dks = _strides(k, packed), _strides(dk_out, packed), _strides(dk, packed)
     elif k_weight is not None:
         raise ValueError("k_weight needs k")
-    rot, max_pos, e, wcode = _rotation_args(q, q_weight, k_weight, rope, eps, d)
-    pos_stride = _positions_args(positions, B, N)
+    rot, max_pos, e, wcode = _rotation_args(q.dtype, q_weight, k_weight, rope, eps, d)
+    pos_stride = _position_stride(positions, B, N)
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
+    strides = _pack18(*_strides(q, packed), *ks, *_strides(dq_out, packed), *kgs, *_strides(dq, packed), *dks)
     ws_bytes = 0
     if dqw is not None or dkw is not None:
         if workspace is None:
             workspace = torch.empty(norm_rope_backward_workspace_size(d), dtype=torch.uint8, device=q.device)
         ws_bytes = workspace.numel() * workspace.element_size()
-    with _On(q.device):
-        st = _lib().fa_norm_rope_backward(
-            _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk),
-            (ctypes.c_longlong * 18)(*qs, *ks, *qgs, *kgs, *_heads_view(dq, "dq")[1], *dks), _ptr(q_weight),
-            _ptr(k_weight), _ptr(dqw), _ptr(dkw), _ptr(rope), _ptr(positions), pos_stride, B, Hq, Hk, N, d, rot, max_pos,
-            e, int(bool(interleaved)), _dtype_code(q.dtype), wcode, _ptr(workspace), ws_bytes, _stream(q.device))
-    _check(st, "fa_norm_rope_backward")
+    _launch(_lib().fa_norm_rope_backward, "fa_norm_rope_backward", device, q.data_ptr(), _addr(k), dq_out.data_ptr(),
+            _addr(dk_out), dq.data_ptr(), _addr(dk), strides, _addr(q_weight), _addr(k_weight), _addr(dqw), _addr(dkw),
+            _addr(rope), _addr(positions), pos_stride, B, Hq, Hk,
+            N, d, rot, max_pos, e, int(bool(interleaved)), _dtype_code(q.dtype), wcode, _addr(workspace), ws_bytes)
     return dq, dk, dqw, dkw
 
 
@@ -690,19 +703,20 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=N
     return _QKNormRope.apply(q, k, q_weight, k_weight, rope, positions, eps, bool(interleaved))
 
 
-def _packed(name, t, H, d, dtype):
+def _token_stride(name, t, T, H, d, dtype):
     """The token stride of a packed [T, H, d] tensor whose heads are contiguous."""
-    if t.dim() != 3 or t.shape[1:] != (H, d) or t.dtype != dtype:
-        raise ValueError(f"{name} must be [T, {H}, {d}] with the pools' dtype")
+    if t.shape != (T, H, d) or t.dtype != dtype:
+        raise ValueError(f"{name} must be packed [{T}, {H}, {d}] with the pools' dtype")
     st = t.stride()
-    if st[2] != 1 or (H > 1 and st[1] != d):
+    if st[2] != 1 or (st[1] != d and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return st[0]
 
 
-def _paged_args(kpool, vpool, block_table, seqlens, cu_tokens, T):
+def _paged_sizes(kpool, vpool, block_table, seqlens, cu_tokens, T):
     """(num_blocks, Hkv, block_size, d, B, max_blocks) of a paged cache, its tensors checked."""
-    if kpool.dim() != 4 or vpool.shape != kpool.shape or vpool.dtype != kpool.dtype:
+    shape = kpool.shape
+    if len(shape) != 4 or vpool.shape != shape or vpool.dtype != kpool.dtype:
         raise ValueError("kpool and vpool must be [num_blocks, Hkv, block_size, d] and share dtype")
     if not (kpool.is_contiguous() and vpool.is_contiguous()):
         raise ValueError("kpool and vpool must be contiguous")
@@ -715,7 +729,7 @@ def _paged_args(kpool, vpool, block_table, seqlens, cu_tokens, T):
         _need_int32("cu_tokens", cu_tokens, (B + 1,))
     elif T != B:
         raise ValueError("without cu_tokens there is one token for each sequence")
-    return (*kpool.shape, B, max_blocks)
+    return (*shape, B, max_blocks)
 
 
 def append_paged(k, v, kpool, vpool, block_table, seqlens, cu_tokens=None, rope=None, q=None, q_weight=None,
@@ -734,33 +748,27 @@ def append_paged(k, v, kpool, vpool, block_table, seqlens, cu_tokens=None, rope=
     A token without a place (position outside the cache or the table, block id outside
     the pool) is not written and reported by device_status().
     """
-    _need_on(k.device, v=v, q=q, q_out=q_out, kpool=kpool, vpool=vpool, block_table=block_table, seqlens=seqlens,
-             cu_tokens=cu_tokens, rope=rope, q_weight=q_weight, k_weight=k_weight)
+    device = _on(k, v, kpool, vpool, block_table, seqlens, cu_tokens, rope, q, q_weight, k_weight, q_out)
     T = k.shape[0]
-    num_blocks, Hkv, bs, d, B, max_blocks = _paged_args(kpool, vpool, block_table, seqlens, cu_tokens, T)
-    k_stride, v_stride = _packed("k", k, Hkv, d, kpool.dtype), _packed("v", v, Hkv, d, kpool.dtype)
-    if v.shape[0] != T:
-        raise ValueError("k and v must have the same tokens")
-    rot, max_pos, e, wcode = _rotation_args(k, q_weight, k_weight, rope, eps, d)
+    dtype = kpool.dtype
+    num_blocks, Hkv, bs, d, B, max_blocks = _paged_sizes(kpool, vpool, block_table, seqlens, cu_tokens, T)
+    k_stride, v_stride = _token_stride("k", k, T, Hkv, d, dtype), _token_stride("v", v, T, Hkv, d, dtype)
+    rot, max_pos, e, wcode = _rotation_args(dtype, q_weight, k_weight, rope, eps, d)
     Hq = q_stride = 0
     if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else 0
-        q_stride = _packed("q", q, Hq, d, kpool.dtype)
-        if q.shape[0] != T:
-            raise ValueError("q and k must have the same tokens")
-        if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous with q's shape and dtype")
+        if q.dim() != 3:
+            raise ValueError("q must be packed [T, Hq, d]")
+        Hq = q.shape[1]
+        q_stride = _token_stride("q", q, T, Hq, d, dtype)
+        q_out = _out_like(q, q_out)
+        if not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous")
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need q")
-    with _On(k.device):
-        st = _lib().fa_append_paged(_ptr(k), _ptr(v), _ptr(q), _ptr(q_out), _ptr(kpool), _ptr(vpool), _ptr(block_table),
-                                    _ptr(cu_tokens), _ptr(seqlens), q_stride, k_stride, v_stride, _ptr(q_weight),
-                                    _ptr(k_weight), _ptr(rope), T, B, Hq, Hkv, num_blocks, bs, max_blocks, d, rot,
-                                    max_pos, e, int(bool(interleaved)), _dtype_code(kpool.dtype), wcode,
-                                    _stream(k.device))
-    _check(st, "fa_append_paged")
+    _launch(_lib().fa_append_paged, "fa_append_paged", device, k.data_ptr(), v.data_ptr(), _addr(q), _addr(q_out),
+            kpool.data_ptr(), vpool.data_ptr(), block_table.data_ptr(), _addr(cu_tokens), seqlens.data_ptr(), q_stride,
+            k_stride, v_stride, _addr(q_weight), _addr(k_weight), _addr(rope), T, B, Hq, Hkv, num_blocks, bs, max_blocks,
+            d, rot, max_pos, e, int(bool(interleaved)), _dtype_code(dtype), wcode)
     return q_out
 
 
@@ -782,31 +790,28 @@ def extend_paged(q, kpool, vpool, block_table, seqlens, cu_tokens=None, causal: 
     may overlap need workspaces of their own (the default makes one).  An out-of-range
     block id of a used block is skipped and reported by device_status().
     """
-    _need_on(q.device, kpool=kpool, vpool=vpool, block_table=block_table, seqlens=seqlens, cu_tokens=cu_tokens,
-             workspace=workspace, out=out, lse=lse)
+    device = _on(q, kpool, vpool, block_table, seqlens, cu_tokens, workspace, out, lse)
     if q.dim() != 3:
         raise ValueError("q must be packed [T, Hq, d]")
     T, Hq = q.shape[:2]
-    num_blocks, Hkv, bs, d, B, max_blocks = _paged_args(kpool, vpool, block_table, seqlens, cu_tokens, T)
-    q_stride = _packed("q", q, Hq, d, kpool.dtype)
+    dtype = kpool.dtype
+    num_blocks, Hkv, bs, d, B, max_blocks = _paged_sizes(kpool, vpool, block_table, seqlens, cu_tokens, T)
+    q_stride = _token_stride("q", q, T, Hq, d, dtype)
     if Hkv < 1 or Hq % Hkv:
         raise ValueError("the query heads must be a multiple of the pools' heads")
-    if out is None:
-        out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-        raise ValueError("out must be contiguous with q's shape and dtype")
+    out = _out_like(q, out)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((T, Hq), dtype=torch.float32)
     elif lse.shape != (T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 tensor [T, Hq]")
     if workspace is None:
-        workspace = torch.empty(max(extend_paged_workspace_size(T, Hq, Hkv, d), 256), dtype=torch.uint8, device=q.device)
-    with _On(q.device):
-        st = _lib().fa_extend_paged(_ptr(q), _ptr(kpool), _ptr(vpool), _ptr(block_table), _ptr(cu_tokens), _ptr(seqlens),
-                                    _ptr(out), _ptr(lse), q_stride, T, B, Hq, Hkv, num_blocks, bs, max_blocks, d,
-                                    _scale_arg(scale), int(bool(causal)), int(window), _dtype_code(q.dtype),
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(q.device))
-    _check(st, "fa_extend_paged")
+        workspace = q.new_empty(max(extend_paged_workspace_size(T, Hq, Hkv, d), 256), dtype=torch.uint8)
+    _launch(_lib().fa_extend_paged, "fa_extend_paged", device, q.data_ptr(), kpool.data_ptr(), vpool.data_ptr(),
+            block_table.data_ptr(), _addr(cu_tokens), seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), q_stride, T, B,
+            Hq, Hkv, num_blocks, bs, max_blocks, d, _scale_arg(scale), int(bool(causal)), int(window),
+            _dtype_code(dtype), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, lse
 
 
