@@ -275,6 +275,7 @@ FA_API fa_status fa_backward(const void* q, const void* k, const void* v, const 
  *   q_out,
  *   k_out      : outputs of the same sizes at strides of their own; an output
  *                may be its input (same pointer and strides).
+ *   B, N       : B * N < 2^31.
  *   strides    : HOST array of 12: (batch, head, row) strides in elements of q, k,
  *                q_out, k_out (k's unread without k).  Each is >= 0 and a
  *                multiple of 16 bytes, and > 0 for the outputs, wherever the

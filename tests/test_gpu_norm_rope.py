@@ -73,6 +73,12 @@ def test_sizes(B, Hq, Hk, N):
     check(q, k, dq, dk, qw, kw, rope, 1e-5, False, table=rope)
 
 
+@pytest.mark.parametrize("Hq,Hk", [(1, 2500), (2500, 1)])
+def test_lopsided_heads(Hq, Hk):
+    q, k, dq, dk, qw, kw, rope = make(1, Hq, Hk, 3, 64, 64, BF16, seed=20)
+    check(q, k, dq, dk, qw, kw, rope, 1e-6, False, table=rope)
+
+
 def test_float32_weights_with_16_bit_rows():
     q, k, dq, dk, qw, kw, rope = make(2, 4, 2, 40, 128, 64, BF16, seed=3, wdtype=FP32)
     check(q, k, dq, dk, qw, kw, rope, 1e-6, False, table=rope)

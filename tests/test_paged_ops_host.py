@@ -36,7 +36,7 @@ def norm_rope(lib, q=GOOD, k=GOOD, qo=GOOD, ko=GOOD, st=None, qw=None, kw=None, 
 @pytest.mark.parametrize("bad", [
     dict(q=None), dict(qo=None), dict(ko=None), dict(k=None), dict(q=MISALIGNED), dict(ko=MISALIGNED),
     dict(qw=MISALIGNED), dict(rope=MISALIGNED), dict(rope=None), dict(pos=P(0x100002)), dict(pos_stride=-1), dict(B=0),
-    dict(Hq=0), dict(Hk=0), dict(N=0), dict(N=(1 << 30) + 1), dict(rot=8), dict(rot=136), dict(rot=-16), dict(rot=0),
+    dict(Hq=0), dict(Hk=0), dict(N=0), dict(N=(1 << 30) + 1), dict(B=3, N=1 << 30), dict(rot=8), dict(rot=136), dict(rot=-16), dict(rot=0),
     dict(max_pos=0), dict(eps=float("nan")), dict(eps=float("inf")), dict(inter=2),
     dict(eps=-1.0, rot=0, rope=None),                                     # neither norm nor rotation
     dict(st=strides(*ROWS * 3, 4 * 10 * 128, 10 * 128, 127)),            # k_out's rows 254 bytes apart

@@ -53,20 +53,20 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
   const int heads = min(HG, (kind == 0 ? a.Hq : a.Hkv) - h0);
   const void* src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
   const long long stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
-  const Lane l = lane_of<D, INTER>(s, a.rot);
+  const Lane l = lane_of<E, D, INTER>(s, a.rot);
 
   uint2 rlo[HG], rhi[HG];
-  const long long x0 = t * stride + static_cast<long long>(h0) * D;
+  const char* x = static_cast<const char*>(src) + (t * stride + static_cast<long long>(h0) * D) * 2;
 #pragma unroll
   for (int h = 0; h < HG; ++h) {
     rlo[h] = rhi[h] = make_uint2(0u, 0u);
     if (live && h < heads) {
-      rlo[h] = load4<E>(src, x0 + h * D + l.lo);
-      rhi[h] = load4<E>(src, x0 + h * D + l.hi);
+      rlo[h] = load4<E>(x + h * D * 2 + l.lo);
+      rhi[h] = load4<E>(x + h * D * 2 + l.hi);
     }
   }
-  float wlo[4], whi[4];
-  if (NORM && kind < 2) load_weight<E>(kind == 0 ? a.q_weight : a.k_weight, a.w_f32, l, wlo, whi);
+  Oct w;
+  if (NORM && kind < 2) w = load_weight<E, D, INTER>(kind == 0 ? a.q_weight : a.k_weight, a.w_f32, s, a.rot);
 
   // The token's place.  A token past the last sequence has none and writes nothing.
   int b = 0;
@@ -96,37 +96,39 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
   }
   if (placed && !good && s == 0) atomicOr(&g_status, kStatusBadBlock);
 
-  float c[4], sn[4];
-  load_angles(a.rope, pos, good, a.rot, s, l.turn && placed && kind < 2, c, sn);
-
   void* dst = kind == 0 ? a.q_out : kind == 1 ? a.kpool : a.vpool;
   const long long row0 = kind == 0 ? t * a.Hq + h0
                                    : ((static_cast<long long>(phys) * a.Hkv + h0) << a.block_shift) +
                                          (pos & ((1 << a.block_shift) - 1));
-  const long long next = kind == 0 ? 1 : 1LL << a.block_shift;
+  const long long next = (kind == 0 ? 1LL : 1LL << a.block_shift) * (D * 2);
+  char* y = static_cast<char*>(dst) + row0 * (D * 2);
+  // A query without a place in the cache or the table comes out NaN where it is rotated.
+  const bool write = kind == 0 ? placed : good;
+  Turn turn;
+  if (kind < 2) {
+    turn = rotation<INTER>(a.rope, pos, good, a.rot, s, l.turn && placed);
+    if (NORM) turn = weighted<INTER>(turn, w);
+  }
 #pragma unroll
   for (int h = 0; h < HG; ++h) {
-    float lo[4], hi[4];
-    unpack4<E>(rlo[h], lo);
-    unpack4<E>(rhi[h], hi);
-    if (NORM && kind < 2) {
-      const float r = 1.f / sqrtf(row_sum<L>(dot8(lo, hi, lo, hi)) * (1.f / D) + a.eps);
+    if (kind < 2) {
+      Oct v = unpack<E>(rlo[h], rhi[h]);
+      if (NORM) {
+        const uint64_t r = f2_both(rsqrt_row(row_sum<L>(dot(v, v)) * (1.f / D) + a.eps));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] *= r * wlo[i];
-        hi[i] *= r * whi[i];
+        for (int i = 0; i < 4; ++i) v.p[i] = f2_mul(v.p[i], r);
+      }
+      if (NORM || l.turn) {
+        const Oct z = apply<INTER>(turn, l.turn, v);
+        rlo[h] = pack<E>(z.p[0], z.p[1]);
+        rhi[h] = pack<E>(z.p[2], z.p[3]);
       }
     }
-    if (kind < 2) {
-      if (l.turn) rotate<INTER>(lo, hi, c, sn);
-      rlo[h] = pack4<E>(lo);
-      rhi[h] = pack4<E>(hi);
+    if (write && h < heads) {
+      store4<E>(y + l.lo, rlo[h]);
+      store4<E>(y + l.hi, rhi[h]);
     }
-    // A query without a place in the cache or the table comes out NaN where it is rotated.
-    if ((kind == 0 ? placed : good) && h < heads) {
-      store4<E>(dst, (row0 + h * next) * D + l.lo, rlo[h]);
-      store4<E>(dst, (row0 + h * next) * D + l.hi, rhi[h]);
-    }
+    y += next;
   }
 }
 

@@ -50,7 +50,8 @@ bool rotation_ok(const float* rope, int d, int rot, int max_pos, float eps, int 
 fa_status norm_rope_args(fa::NormRopeArgs& a, const void* q_weight, const void* k_weight, const float* rope,
                          const int32_t* positions, long long pos_stride, int B, int Hq, int Hk, int N, int d,
                          int rot, int max_pos, float eps, int interleaved, fa_dtype dtype, fa_dtype weight_dtype) {
-  if (!sizes_ok(B, Hq, N) || (Hk != 0 && !sizes_ok(B, Hk, N))) return FA_ERR_INVALID;
+  if (!sizes_ok(B, Hq, N) || (Hk != 0 && !sizes_ok(B, Hk, N)) || static_cast<long long>(B) * N > 0x7fffffffLL)
+    return FA_ERR_INVALID;
   if (!rotation_ok(rope, d, rot, max_pos, eps, interleaved) || (eps < 0.f && rot == 0)) return FA_ERR_INVALID;
   if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 4) || pos_stride < 0 ||
       pos_stride > (1LL << 42))
@@ -297,7 +298,7 @@ fa_status fa_norm_rope(const void* q, const void* k, void* q_out, void* k_out, c
 
 size_t fa_norm_rope_backward_workspace_size(int d) {
   if (d != 64 && d != 128) return 0;
-  return static_cast<size_t>(fa::kNormRopeBlocks) * 2 * d * sizeof(float);
+  return static_cast<size_t>(fa::kNormRopeBlocks) * d * sizeof(float);
 }
 
 fa_status fa_norm_rope_backward(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk,

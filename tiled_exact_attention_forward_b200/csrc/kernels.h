@@ -92,7 +92,7 @@ struct NormRopeArgs {
   float eps;
   int norm, interleaved;
   int f16, f32, w_f32;
-  float* partials;              // backward with dw: [kNormRopeBlocks][2][d]
+  float* partials;              // backward with dw: [kNormRopeBlocks][d]
 };
 
 // Blocks of the backward's persistent grid (148 SMs x 4 resident blocks).  A constant,

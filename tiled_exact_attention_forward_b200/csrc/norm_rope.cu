@@ -6,7 +6,7 @@
 // where R(p) turns the first `rot` elements pairwise by the table's angles.
 // Backward, with dz given:
 //   g = R(p)^T dz,  dw = sum over rows of g x r,  u = g w,
-//   dx = r (u - x r^2 mean(u x)).
+//   dx = r u - x r^3 mean(u x).
 // r is recomputed from x (which the backward reads anyway) instead of being saved.
 // All arithmetic is float32; each output is rounded once.
 //
@@ -29,236 +29,215 @@ namespace nrope {
 using namespace rows;
 
 constexpr int THREADS = 256;
-constexpr int HG = 4;  // heads per group of lanes
+// Heads per group of lanes: 64 bytes a lane in flight per tensor read.
+template <class E> __host__ __device__ constexpr int heads_per_group() { return 8 / elem_bytes<E>(); }
 
 template <int D> __host__ __device__ constexpr int positions_per_block() { return THREADS / (D / 8); }
 
-// A block's work: HG heads of tensor t (0 = q, 1 = k) from head h0 on, for the
-// positions [p0, p0 + positions_per_block).
-struct Tile {
-  int t, h0, heads;
-  long long p0;
+// A lane's place: row n of batch b, from the row's number among all B * N.
+struct Place {
+  unsigned b, n;
 };
-template <int D> __device__ __forceinline__ Tile tile_of(long long i, const NormRopeArgs& a) {
-  const int gq = (a.H[0] + HG - 1) / HG, gk = (a.H[1] + HG - 1) / HG;
-  const int hg = static_cast<int>(i % (gq + gk));
-  Tile w;
-  w.p0 = (i / (gq + gk)) * positions_per_block<D>();
-  w.t = hg < gq ? 0 : 1;
-  w.h0 = (hg < gq ? hg : hg - gq) * HG;
-  w.heads = min(HG, a.H[w.t] - w.h0);
-  return w;
+__device__ __forceinline__ Place place_of(const NormRopeArgs& a, unsigned p) {
+  const unsigned b = a.B == 1 ? 0u : p / static_cast<unsigned>(a.N);
+  return Place{b, p - b * static_cast<unsigned>(a.N)};
 }
-
-// The angles of row n of batch b.
-__device__ __forceinline__ void angles(const NormRopeArgs& a, long long b, long long n, bool live, int s, const Lane& l,
-                                       float (&c)[4], float (&sn)[4]) {
-  const long long pos = a.positions && live ? a.positions[b * a.pos_stride + n] : n;
+template <bool INTER>
+__device__ __forceinline__ Turn rotation_at(const NormRopeArgs& a, const Place& at, bool live, int s, bool turn) {
+  const long long pos = a.positions && live ? a.positions[at.b * a.pos_stride + at.n] : at.n;
   const bool inside = pos >= 0 && pos < a.max_pos;
-  if (l.turn && live && !inside) atomicOr(&g_status, kStatusBadBlock);
-  load_angles(a.rope, pos, inside, a.rot, s, l.turn && live, c, sn);
+  if (turn && live && !inside) atomicOr(&g_status, kStatusBadBlock);
+  return rotation<INTER>(a.rope, pos, inside, a.rot, s, turn && live);
+}
+template <class E>
+__device__ __forceinline__ const char* row_at(const void* base, const long long (&stride)[3], const Place& at, int h) {
+  return static_cast<const char*>(base) + (at.b * stride[0] + h * stride[1] + at.n * stride[2]) * elem_bytes<E>();
 }
 
+// blockIdx.x: the head groups of a run of positions come one after another.
 template <class E, int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
-  constexpr int L = D / 8;
+  constexpr int L = D / 8, HG = heads_per_group<E>();
   const int s = threadIdx.x % L;
-  const Tile w = tile_of<D>(blockIdx.x, a);
-  const long long p = w.p0 + threadIdx.x / L;
-  const bool live = p < static_cast<long long>(a.B) * a.N;
-  const Lane l = lane_of<D, INTER>(s, a.rot);
-  const long long b = live ? p / a.N : 0, n = live ? p - b * a.N : 0;
+  const unsigned gq = (a.H[0] + HG - 1) / HG, groups = gq + (a.H[1] + HG - 1) / HG;
+  const unsigned tile = blockIdx.x / groups, hg = blockIdx.x - tile * groups;
+  const int t = hg < gq ? 0 : 1;
+  const int h0 = (t ? hg - gq : hg) * HG, heads = min(HG, a.H[t] - h0);
+  const unsigned p = tile * positions_per_block<D>() + threadIdx.x / L;
+  const bool live = p < static_cast<unsigned>(a.B) * static_cast<unsigned>(a.N);
+  const Place at = place_of(a, live ? p : 0u);
+  const Lane l = lane_of<E, D, INTER>(s, a.rot);
 
-  const long long* xs = a.x_stride[w.t];
-  const long long x0 = b * xs[0] + w.h0 * xs[1] + n * xs[2];
+  const char* x = row_at<E>(a.x[t], a.x_stride[t], at, h0);
+  const long long xh = a.x_stride[t][1] * elem_bytes<E>();
   typename Raw<E>::type rlo[HG], rhi[HG];
 #pragma unroll
-  for (int h = 0; h < HG; ++h)
-    if (live && h < w.heads) {
-      rlo[h] = load4<E>(a.x[w.t], x0 + h * xs[1] + l.lo);
-      rhi[h] = load4<E>(a.x[w.t], x0 + h * xs[1] + l.hi);
-    } else {
-      rlo[h] = rhi[h] = typename Raw<E>::type{};
+  for (int h = 0; h < HG; ++h) {
+    rlo[h] = rhi[h] = typename Raw<E>::type{};
+    if (live && h < heads) {
+      rlo[h] = load4<E>(x + l.lo);
+      rhi[h] = load4<E>(x + l.hi);
     }
-  float c[4], sn[4], wlo[4], whi[4];
-  angles(a, b, n, live, s, l, c, sn);
-  if (NORM) load_weight<E>(a.w[w.t], a.w_f32, l, wlo, whi);
+    x += xh;
+  }
+  Turn turn = rotation_at<INTER>(a, at, live, s, l.turn);
+  if (NORM) turn = weighted<INTER>(turn, load_weight<E, D, INTER>(a.w[t], a.w_f32, s, a.rot));
 
-  const long long* ys = a.y_stride[w.t];
-  const long long y0 = b * ys[0] + w.h0 * ys[1] + n * ys[2];
+  char* y = const_cast<char*>(row_at<E>(a.y[t], a.y_stride[t], at, h0));
+  const long long yh = a.y_stride[t][1] * elem_bytes<E>();
 #pragma unroll
   for (int h = 0; h < HG; ++h) {
-    float lo[4], hi[4];
-    unpack4<E>(rlo[h], lo);
-    unpack4<E>(rhi[h], hi);
+    Oct v = unpack<E>(rlo[h], rhi[h]);
     if (NORM) {
-      const float r = 1.f / sqrtf(row_sum<L>(dot8(lo, hi, lo, hi)) * (1.f / D) + a.eps);
+      const uint64_t r = f2_both(rsqrt_row(row_sum<L>(dot(v, v)) * (1.f / D) + a.eps));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] *= r * wlo[i];
-        hi[i] *= r * whi[i];
-      }
+      for (int i = 0; i < 4; ++i) v.p[i] = f2_mul(v.p[i], r);
     }
-    if (l.turn) rotate<INTER>(lo, hi, c, sn);
-    if (live && h < w.heads) {
-      store4<E>(a.y[w.t], y0 + h * ys[1] + l.lo, pack4<E>(lo));
-      store4<E>(a.y[w.t], y0 + h * ys[1] + l.hi, pack4<E>(hi));
+    const Oct z = apply<INTER>(turn, l.turn, v);
+    if (live && h < heads) {
+      store4<E>(y + l.lo, pack<E>(z.p[0], z.p[1]));
+      store4<E>(y + l.hi, pack<E>(z.p[2], z.p[3]));
     }
+    y += yh;
   }
 }
 
-// Backward.  A persistent grid: each block walks tiles gridDim.x apart and keeps its
-// share of dw in registers, so the weight gradients cost one partial row per block;
-// sum_partials_kernel adds the blocks' rows in a fixed order (no atomics: the result
-// does not depend on timing).
+// Backward.  A persistent grid, the first `blocks_q` blocks for q, the rest for k: each
+// block walks its tensor's tiles a grid's share apart and keeps its part of dw in
+// registers, so the weight gradients cost one partial row per block, which
+// sum_partials_kernel adds in a fixed order (no atomics: the result does not depend on
+// timing).
 template <class E, int D, bool INTER, bool NORM>
-__global__ void __launch_bounds__(THREADS) norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, long long tiles) {
-  constexpr int L = D / 8, P = positions_per_block<D>();
+__global__ void __launch_bounds__(THREADS)
+    norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, unsigned tiles, unsigned blocks_q) {
+  constexpr int L = D / 8, P = positions_per_block<D>(), HG = heads_per_group<E>();
   const int s = threadIdx.x % L;
-  const Lane l = lane_of<D, INTER>(s, a.rot);
-  float dw[2][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
+  const Lane l = lane_of<E, D, INTER>(s, a.rot);
+  const int t = blockIdx.x < blocks_q ? 0 : 1;
+  const unsigned first = t ? blockIdx.x - blocks_q : blockIdx.x, step = t ? gridDim.x - blocks_q : blocks_q;
+  const unsigned groups = (a.H[t] + HG - 1) / HG;
+  const long long xh = a.x_stride[t][1] * elem_bytes<E>(), gh = a.g_stride[t][1] * elem_bytes<E>(),
+                  yh = a.y_stride[t][1] * elem_bytes<E>();
+  Oct w;
+  if (NORM) w = load_weight<E, D, INTER>(a.w[t], a.w_f32, s, a.rot);
+  uint64_t dw[4] = {0, 0, 0, 0};
 
-  for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
-    const Tile w = tile_of<D>(i, a);
-    const long long p = w.p0 + threadIdx.x / L;
-    const bool live = p < static_cast<long long>(a.B) * a.N;
-    const long long b = live ? p / a.N : 0, n = live ? p - b * a.N : 0;
-    const long long* xs = a.x_stride[w.t];
-    const long long* gs = a.g_stride[w.t];
-    const long long x0 = b * xs[0] + w.h0 * xs[1] + n * xs[2];
-    const long long g0 = b * gs[0] + w.h0 * gs[1] + n * gs[2];
+  for (unsigned i = first; i < tiles * groups; i += step) {
+    const unsigned tile = i / groups;
+    const int h0 = (i - tile * groups) * HG, heads = min(HG, a.H[t] - h0);
+    const unsigned p = tile * P + threadIdx.x / L;
+    const bool live = p < static_cast<unsigned>(a.B) * static_cast<unsigned>(a.N);
+    const Place at = place_of(a, live ? p : 0u);
+    const char* x = NORM ? row_at<E>(a.x[t], a.x_stride[t], at, h0) : nullptr;
+    const char* g = row_at<E>(a.g[t], a.g_stride[t], at, h0);
     typename Raw<E>::type xlo[HG], xhi[HG], glo[HG], ghi[HG];
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
+      // A dead row or head reads as zeros and adds zeros to dw.
       xlo[h] = xhi[h] = glo[h] = ghi[h] = typename Raw<E>::type{};
-      if (live && h < w.heads) {
-        glo[h] = load4<E>(a.g[w.t], g0 + h * gs[1] + l.lo);
-        ghi[h] = load4<E>(a.g[w.t], g0 + h * gs[1] + l.hi);
+      if (live && h < heads) {
+        glo[h] = load4<E>(g + l.lo);
+        ghi[h] = load4<E>(g + l.hi);
         if (NORM) {
-          xlo[h] = load4<E>(a.x[w.t], x0 + h * xs[1] + l.lo);
-          xhi[h] = load4<E>(a.x[w.t], x0 + h * xs[1] + l.hi);
+          xlo[h] = load4<E>(x + l.lo);
+          xhi[h] = load4<E>(x + l.hi);
         }
       }
+      g += gh;
+      if (NORM) x += xh;
     }
-      float c[4], sn[4], wlo[4], whi[4];
-    angles(a, b, n, live, s, l, c, sn);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sn[e] = -sn[e];
-    if (NORM) load_weight<E>(a.w[w.t], a.w_f32, l, wlo, whi);
+    const Turn back = transposed(rotation_at<INTER>(a, at, live, s, l.turn));
 
-    const long long* ys = a.y_stride[w.t];
-    const long long y0 = b * ys[0] + w.h0 * ys[1] + n * ys[2];
+    char* y = const_cast<char*>(row_at<E>(a.y[t], a.y_stride[t], at, h0));
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
-      float lo[4], hi[4];
-      unpack4<E>(glo[h], lo);
-      unpack4<E>(ghi[h], hi);
-      if (l.turn) rotate<INTER>(lo, hi, c, sn);
+      Oct v = apply<INTER>(back, l.turn, unpack<E>(glo[h], ghi[h]));  // g
       if (NORM) {
-        float x1[4], x2[4], u1[4], u2[4];
-        unpack4<E>(xlo[h], x1);
-        unpack4<E>(xhi[h], x2);
-        const float r = 1.f / sqrtf(row_sum<L>(dot8(x1, x2, x1, x2)) * (1.f / D) + a.eps);
+        const Oct xv = unpack<E>(xlo[h], xhi[h]);
+        Oct gx;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gx.p[e] = f2_mul(v.p[e], xv.p[e]);
+        const float ss = row_sum<L>(dot(xv, xv)), ux = row_sum<L>(dot(gx, w));
+        // A dead row's r is 1 / sqrt(eps), infinite for eps = 0: kept out of dw.
+        const float r = live && h < heads ? rsqrt_row(ss * (1.f / D) + a.eps) : 0.f;
+        const uint64_t r2 = f2_both(r), c2 = f2_both(-r * r * r * (ux * (1.f / D)));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x1[e] *= r;  // the normalised row
-          x2[e] *= r;
-          u1[e] = lo[e] * wlo[e];
-          u2[e] = hi[e] * whi[e];
-        }
-        // A dead row or head adds nothing: its g is zero, its r finite or multiplied by zero.
-        const bool count = live && h < w.heads;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float d1 = count ? lo[e] * x1[e] : 0.f, d2 = count ? hi[e] * x2[e] : 0.f;
-          if (w.t == 0) {
-            dw[0][e] += d1;
-            dw[0][4 + e] += d2;
-          } else {
-            dw[1][e] += d1;
-            dw[1][4 + e] += d2;
-          }
-        }
-        const float m = row_sum<L>(dot8(u1, u2, x1, x2)) * (1.f / D);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          lo[e] = r * (u1[e] - x1[e] * m);
-          hi[e] = r * (u2[e] - x2[e] * m);
+          dw[e] = f2_fma(gx.p[e], r2, dw[e]);
+          v.p[e] = f2_fma(xv.p[e], c2, f2_mul(v.p[e], f2_mul(w.p[e], r2)));
         }
       }
-      if (live && h < w.heads) {
-        store4<E>(a.y[w.t], y0 + h * ys[1] + l.lo, pack4<E>(lo));
-        store4<E>(a.y[w.t], y0 + h * ys[1] + l.hi, pack4<E>(hi));
+      if (live && h < heads) {
+        store4<E>(y + l.lo, pack<E>(v.p[0], v.p[1]));
+        store4<E>(y + l.hi, pack<E>(v.p[2], v.p[3]));
       }
+      y += yh;
     }
   }
 
   if (NORM && a.partials != nullptr) {
     __shared__ float sm[P][D];
+    const Lane e = lane_of<F32, D, INTER>(s, a.rot);
+    char* row = reinterpret_cast<char*>(sm[threadIdx.x / L]);
+    store4<F32>(row + e.lo, pack<F32>(dw[0], dw[1]));
+    store4<F32>(row + e.hi, pack<F32>(dw[2], dw[3]));
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float v = 0.f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if (t) __syncthreads();
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sm[threadIdx.x / L][l.lo + e] = dw[t][e];
-        sm[threadIdx.x / L][l.hi + e] = dw[t][4 + e];
-      }
-      __syncthreads();
-      if (threadIdx.x < D) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < P; ++i) v += sm[i][threadIdx.x];
-        a.partials[(static_cast<long long>(blockIdx.x) * 2 + t) * D + threadIdx.x] = v;
-      }
+      for (int i = 0; i < P; ++i) v += sm[i][threadIdx.x];
+      a.partials[blockIdx.x * D + threadIdx.x] = v;
     }
   }
 }
 
-// dw[t][e] = sum over the blocks of their partial rows: a block adds 32 columns, 32
-// threads to a column, each over every 32nd block.
+// dw = the sum of the blocks' partial rows, q's blocks then k's: a block adds 32 columns
+// of one of the two, 32 threads to a column, each over every 32nd block.
 template <class E>
-__global__ void __launch_bounds__(1024) sum_partials_kernel(const __grid_constant__ NormRopeArgs a, int blocks) {
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31);  // over [2][d]
-  const int part = threadIdx.x >> 5;
+__global__ void __launch_bounds__(1024) sum_partials_kernel(const __grid_constant__ NormRopeArgs a, int blocks_q, int blocks) {
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5, t = blockIdx.y;
+  if (a.dw[t] == nullptr) return;
+  const int end = t ? blocks : blocks_q;
   float v = 0.f;
-  for (int i = part; i < blocks; i += 32) v += a.partials[static_cast<long long>(i) * 2 * a.d + col];
+#pragma unroll 4
+  for (int i = (t ? blocks_q : 0) + part; i < end; i += 32) v += a.partials[i * a.d + col];
   __shared__ float sm[32][33];
   sm[part][threadIdx.x & 31] = v;
   __syncthreads();
   if (part == 0) {
-    float t = 0.f;
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) t += sm[i][threadIdx.x];
-    const int which = col / a.d, e = col % a.d;
-    if (a.dw[which] != nullptr) {
-      if (a.w_f32) {
-        static_cast<float*>(a.dw[which])[e] = t;
-      } else if constexpr (elem_bytes<E>() == 2) {
-        static_cast<unsigned short*>(a.dw[which])[e] = to16<E>(t);
-      }
+    for (int i = 0; i < 32; ++i) sum += sm[i][threadIdx.x];
+    if (a.w_f32) {
+      static_cast<float*>(a.dw[t])[col] = sum;
+    } else if constexpr (elem_bytes<E>() == 2) {
+      static_cast<unsigned short*>(a.dw[t])[col] = to16<E>(sum);
     }
   }
 }
 
 template <class E, int D, bool INTER>
 cudaError_t launch(const NormRopeArgs& a, bool backward, cudaStream_t stream) {
+  constexpr int HG = heads_per_group<E>();
   const long long positions = static_cast<long long>(a.B) * a.N;
-  const long long groups = (a.H[0] + HG - 1) / HG + (a.H[1] + HG - 1) / HG;
-  const long long tiles = (positions + positions_per_block<D>() - 1) / positions_per_block<D>() * groups;
-  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long tiles = (positions + positions_per_block<D>() - 1) / positions_per_block<D>();
+  const long long gq = (a.H[0] + HG - 1) / HG, gk = (a.H[1] + HG - 1) / HG;
+  if (positions > 0x7fffffffLL || tiles * (gq + gk) > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (!backward) {
     (a.norm ? norm_rope_kernel<E, D, INTER, true> : norm_rope_kernel<E, D, INTER, false>)
-        <<<static_cast<unsigned>(tiles), THREADS, 0, stream>>>(a);
+        <<<static_cast<unsigned>(tiles * (gq + gk)), THREADS, 0, stream>>>(a);
     return cudaGetLastError();
   }
-  const unsigned grid = static_cast<unsigned>(tiles < kNormRopeBlocks ? tiles : kNormRopeBlocks);
+  // Blocks in proportion to the tensors' tiles, at least one each.
+  const long long all = tiles * (gq + gk) < kNormRopeBlocks ? tiles * (gq + gk) : kNormRopeBlocks;
+  long long bk = gk == 0 ? 0 : (all * gk + gq + gk - 1) / (gq + gk);
+  if (bk > all - 1) bk = all - 1;
+  const unsigned blocks_q = static_cast<unsigned>(all - bk), blocks = static_cast<unsigned>(all);
   (a.norm ? norm_rope_bwd_kernel<E, D, INTER, true> : norm_rope_bwd_kernel<E, D, INTER, false>)
-      <<<grid, THREADS, 0, stream>>>(a, tiles);
+      <<<blocks, THREADS, 0, stream>>>(a, static_cast<unsigned>(tiles), blocks_q);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.norm || a.partials == nullptr) return e;
-  sum_partials_kernel<E><<<2 * D / 32, 1024, 0, stream>>>(a, static_cast<int>(grid));
+  sum_partials_kernel<E><<<dim3(D / 32, gk ? 2 : 1), 1024, 0, stream>>>(a, static_cast<int>(blocks_q), static_cast<int>(blocks));
   return cudaGetLastError();
 }
 
