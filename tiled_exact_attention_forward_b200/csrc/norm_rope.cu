@@ -28,7 +28,7 @@ namespace nrope {
 
 using namespace rows;
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 // Heads per group of lanes: 64 bytes a lane in flight per tensor read.
 template <class E> __host__ __device__ constexpr int heads_per_group() { return 8 / elem_bytes<E>(); }
 
@@ -111,6 +111,7 @@ template <class E, int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(THREADS)
     norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, unsigned tiles, unsigned blocks_q) {
   constexpr int L = D / 8, P = positions_per_block<D>(), HG = heads_per_group<E>();
+  let_next_kernel_start();
   const int s = threadIdx.x % L;
   const Lane l = lane_of<E, D, INTER>(s, a.rot);
   const int t = blockIdx.x < blocks_q ? 0 : 1;
@@ -196,6 +197,7 @@ __global__ void __launch_bounds__(THREADS)
 template <class E>
 __global__ void __launch_bounds__(1024) sum_partials_kernel(const __grid_constant__ NormRopeArgs a, int blocks_q, int blocks) {
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5, t = blockIdx.y;
+  wait_for_previous_kernel();
   if (a.dw[t] == nullptr) return;
   const int end = t ? blocks : blocks_q;
   float v = 0.f;
@@ -237,8 +239,8 @@ cudaError_t launch(const NormRopeArgs& a, bool backward, cudaStream_t stream) {
       <<<blocks, THREADS, 0, stream>>>(a, static_cast<unsigned>(tiles), blocks_q);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.norm || a.partials == nullptr) return e;
-  sum_partials_kernel<E><<<dim3(D / 32, gk ? 2 : 1), 1024, 0, stream>>>(a, static_cast<int>(blocks_q), static_cast<int>(blocks));
-  return cudaGetLastError();
+  return launch_dependent(sum_partials_kernel<E>, dim3(D / 32, gk ? 2 : 1), dim3(1024), stream, a,
+                          static_cast<int>(blocks_q), static_cast<int>(blocks));
 }
 
 template <class E>
