@@ -21,7 +21,7 @@ using namespace rows;
 
 constexpr int D = 128;
 constexpr int L = D / 8;
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 constexpr int TOKENS = THREADS / L;  // tokens per block
 constexpr int HG = 4;                // heads per group of lanes
 
