@@ -17,9 +17,9 @@
 //                 S -> softmax -> PV chain of one key tile overlaps the next one's;
 //                 the epilogue joins the two states.
 //
-// Work split.  One persistent CTA per SM.  An item costs one unit for itself and one
-// per key tile; all items laid end to end are cut into equal runs of units, one per
-// CTA, whatever the lengths: a long sequence with few rows is spread over many CTAs,
+// Work split.  One persistent CTA per SM.  Items and their key tiles cost units (Cost
+// below); all items laid end to end are cut into equal runs of units, one per CTA,
+// whatever the lengths: a long sequence with few rows is spread over many CTAs,
 // many short ones share a CTA.  An item cut by a run's edge leaves normalised float32
 // partials and their logsumexp in the workspace, and combine_kernel joins them (in
 // the order of the keys: the result does not depend on timing).  Every CTA works the
@@ -60,11 +60,15 @@ static_assert(2 * WG_THREADS * kSoftmaxRegs + WG_THREADS * kEpilogueRegs + WG_TH
                   NUM_THREADS * kLaunchRegs,
               "register split exceeds the launch budget");
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
-// A CTA takes at least this many units, so that few keys are not scattered over so
-// many CTAs that joining them costs more than it saves.
+// Costs in units of about 0.7 us, from a fit of the CTAs' times on mixed batches: a key
+// tile of a one-tile item 1.3-1.5 us (its bytes at the memory's rate), of a two-tile item
+// 1.8-2.9 us, an item itself 2-3.6 us and 5 us.  A CTA takes at least kMinUnits, so that few
+// keys are not scattered over so many CTAs that joining them costs more than it saves.
+struct Cost {
+  int item, tile;
+};
+constexpr int kItemUnits1 = 4, kTileUnits1 = 2, kItemUnits2 = 7, kTileUnits2 = 3;  // items of one, two row tiles
 constexpr int kMinUnits = 6;
-constexpr int kItemUnits = 5;
-constexpr int kPairUnits = 1;
 // Epilogue: up to so many rows of a warp are written by their own lanes; more go through
 // shared memory, so that a store instruction does not touch 32 lines.
 constexpr int kDirectRows = 8;
@@ -148,13 +152,14 @@ __device__ __forceinline__ int item_tiles(const ExtendArgs& a, const Geo& g, con
   key_range(a, s.n - s.nq + i0, s.n - s.nq + i1 - 1, s.n, lo, hi);
   return hi > lo ? (hi + BN - 1) / BN - lo / BN : 0;
 }
-// Units of a key tile of item p, and of the whole item with nt key tiles.
-__device__ __forceinline__ int tile_units(const Geo& g, const Seq& s, int p) {
-  return s.nq - p * 2 * g.tpt > g.tpt ? kPairUnits : 1;
+// Costs of item p of the sequence, and its units.
+__device__ __forceinline__ Cost cost_of(const Geo& g, const Seq& s, int p) {
+  return s.nq - p * 2 * g.tpt > g.tpt ? Cost{kItemUnits2, kTileUnits2} : Cost{kItemUnits1, kTileUnits1};
 }
 __device__ __forceinline__ int item_units(const ExtendArgs& a, const Geo& g, const Seq& s, int p) {
   int lo, hi;
-  return kItemUnits + item_tiles(a, g, s, p, lo, hi) * tile_units(g, s, p);
+  const Cost c = cost_of(g, s, p);
+  return c.item + item_tiles(a, g, s, p, lo, hi) * c.tile;
 }
 __device__ __forceinline__ int items_of(const Geo& g, int nq) { return (nq + 2 * g.tpt - 1) / (2 * g.tpt); }
 
@@ -474,14 +479,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         long long u0 = u_begin - rem;  // the item's first unit
         while (ok && u0 < u_end) {
           const int nt = item_tiles(args, geo, s, p, lo, hi);
-          // Tile k of the item begins at unit u0 + kItemUnits + k * w, and the run that holds
+          // Tile k of the item begins at unit u0 + c.item + k c.tile, and the run that holds
           // this unit takes it; unit u0 only says who writes an item without keys.
-          const int w = tile_units(geo, s, p);
+          const Cost c = cost_of(geo, s, p);
+          const long long t0 = u0 + c.item;
           auto tile_at = [&](long long u) {
-            const long long k = (u - u0 - kItemUnits + w - 1) / w;
-            return static_cast<int>(min(max(k, 0LL), static_cast<long long>(nt)));
+            return static_cast<int>(min(max((u - t0 + c.tile - 1) / c.tile, 0LL), static_cast<long long>(nt)));
           };
-          const int k0 = u_begin <= u0 + kItemUnits ? 0 : tile_at(u_begin), k1 = u_end <= u0 + kItemUnits ? 0 : tile_at(u_end);
+          const int k0 = u_begin <= t0 ? 0 : tile_at(u_begin), k1 = u_end <= t0 ? 0 : tile_at(u_end);
           if (k0 < k1 || (nt == 0 && u0 >= u_begin)) {
             Piece out;
             const int i0 = p * 2 * geo.tpt;
@@ -497,10 +502,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             out.slot = k0 == 0 && k1 == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (k0 == 0 ? 1 : 0);
             out.stop = 0;
             out.pad = 0;
-            if (k0 == 0 && k1 < nt) open = ExtendDesc{out.tok0, out.ntok, h, static_cast<int>((u0 + kItemUnits + (nt - 1) * w) / run)};
+            if (k0 == 0 && k1 < nt) open = ExtendDesc{out.tok0, out.ntok, h, static_cast<int>((t0 + static_cast<long long>(nt - 1) * c.tile) / run)};
             ok = hand_out(out);
           }
-          u0 += kItemUnits + nt * w;
+          u0 = t0 + nt * c.tile;
           if (++p >= items_of(geo, s.nq)) {
             p = 0;
             if (++h >= args.Hkv) {
