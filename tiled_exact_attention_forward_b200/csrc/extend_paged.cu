@@ -69,20 +69,30 @@ struct Cost {
 };
 constexpr int kItemUnits1 = 4, kTileUnits1 = 2, kItemUnits2 = 7, kTileUnits2 = 3;  // items of one, two row tiles
 constexpr int kMinUnits = 6;
+// Up to so many sequences the planner warp finds the CTA's run alone; for more the whole
+// block does, ahead of everything else.
+constexpr int kPlanSeqs = 128;
 // Epilogue: up to so many rows of a warp are written by their own lanes; more go through
 // shared memory, so that a store instruction does not touch 32 lines.
 constexpr int kDirectRows = 8;
 
 // A run of key tiles [j0, j1) of one item, as the planner hands it to the other warps.
+// Arrays go by slot: a one-tile item's tiles take the slots in turn, through the items
+// (the CTA's tile number g goes to slot g % 2); a two-tile item's row tiles have one each.
 struct Piece {
-  int tok0, ntok;      // the item's tokens in the packed batch
-  int pos0;            // position of the first one in its sequence
-  int kvh, b;
   int j0, j1;
-  int key_lo, key_hi;  // keys of the sequence that some row of the item sees
-  int slot;            // workspace slot of the partial result, -1: the piece is the whole item
-  int stop;            // no more pieces
+  int single;                  // one row tile
+  int stop;                    // no more pieces
+  int b, kvh;
+  int key_lo, key_hi;          // keys of the sequence that some row of the item sees
+  int tok0, ntok;              // the item's tokens in the packed batch
+  int slot;                    // workspace slot of the partial result, -1: the piece is the whole item
   int pad;
+  int first[2], end[2];        // key tiles of the slot: first, end; every second one of a one-tile item
+  int rows[2];                 // rows of the slot's row tile that hold a token
+  int pos[2];                  // position of its first token
+  int all_lo[2], all_hi[2];    // keys that every row of it sees
+  __device__ __forceinline__ bool any(int t) const { return first[t] < end[t]; }
 };
 
 // Dynamic shared memory, 1024-byte aligned: Q tiles, K ring, V ring, then the epilogue's
@@ -98,34 +108,42 @@ struct Geo {
   int G, tpt;
 };
 
+struct Seq {
+  int tok0, nq, n;  // first packed token, new tokens, keys
+};
+// A CTA's run of units [begin, end) of `length` (the last one's may be shorter), and the
+// sequence in which it starts: its number, units before it and units per key head.
+struct Run {
+  long long begin, end, length;
+  long long before, per_head;
+  int b;
+  Seq seq;
+};
+
 // Everything else sits in static shared memory, whose addresses are constants: pointers
 // to it cost no registers.
 struct Ctl {
   uint32_t bad[4][BN / 32];          // keys of a tile whose block lies outside the pool
   Piece piece[NP];
-  uint64_t piece_full[NP], piece_empty[NP];
+  // Barriers, by the arrivals that they count: one, a warpgroup's, the piece readers'.
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[NS], k_empty[NS];
   uint64_t v_full[NS], v_empty[NS];
-  uint64_t s_full[2];
-  uint64_t p_full[2];
-  uint64_t o_full[2], o_free[2];
-  uint64_t st_full[2], st_empty[2];
+  uint64_t s_full[2], o_full[2];
+  uint64_t piece_full[NP];
   uint64_t mma_done;
+  uint64_t p_full[2], o_free[2];
+  uint64_t st_full[2], st_empty[2];
+  uint64_t piece_empty[NP];
   float stat_m[2][BM], stat_l[2][BM];
   long long scan[WARPS];
-  long long start_unit;              // units before the sequence the run starts in
-  long long start_units;             // its units per key head
-  int start_b;                       // that sequence
+  Run run;
   Geo geo;
   uint32_t tmem_base;
   int abort_flag;
 };
 static_assert(kSmemBytes + sizeof(Ctl) + 64 <= 227 * 1024, "shared memory");
 
-struct Seq {
-  int tok0, nq, n;  // first packed token, new tokens, keys
-};
 __device__ __forceinline__ Seq seq_of(const ExtendArgs& a, int b) {
   Seq s;
   if (a.cu_tokens == nullptr) {
@@ -186,27 +204,34 @@ __device__ __forceinline__ long long head_units(const ExtendArgs& a, const Geo& 
   return u;
 }
 
-// The key tiles of piece p that slot t works on: first, end (exclusive) and step; `base`:
-// key tiles of the CTA's pieces before p.  One-tile items' tiles take the slots in turn,
-// through the items: the CTA's tile number g goes to slot g % 2.
-struct Tiles {
-  int first, end, step;
-  __device__ __forceinline__ bool any() const { return first < end; }
-  __device__ __forceinline__ bool has(int j) const { return j >= first && j < end; }  // two-tile items only
-};
-__device__ __forceinline__ bool one_tile(const Geo& g, const Piece& p) { return p.ntok <= g.tpt; }
-__device__ __forceinline__ Tiles slot_tiles(const ExtendArgs& a, const Geo& g, const Piece& p, int t, int base) {
-  if (one_tile(g, p)) return Tiles{p.j0 + ((t ^ base) & 1), p.j1, 2};
-  const int i0 = t * g.tpt, i1 = min(p.ntok, i0 + g.tpt);
-  int lo = p.key_lo, hi = p.key_hi;
-  if (a.causal) hi = min(hi, p.pos0 + i1);
-  if (a.window > 0) lo = max(lo, p.pos0 + i0 - a.window + 1);
-  if (hi <= lo) return Tiles{p.j0, p.j0, 1};
-  return Tiles{max(p.j0, lo / BN), min(p.j1, (hi + BN - 1) / BN), 1};
-}
-// Rows of row tile t that hold a token.
-__device__ __forceinline__ int tile_rows(const Geo& g, const Piece& p, int t) {
-  return max(0, min(p.ntok - t * g.tpt, g.tpt)) * g.G;
+// The piece's fields by slot; `base`: key tiles of the CTA's pieces before it, pos0: the
+// position of its first token.
+__device__ __forceinline__ void fill_slots(const ExtendArgs& a, const Geo& g, Piece& p, int pos0, int base) {
+  p.single = p.ntok <= g.tpt;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int i0 = p.single ? 0 : t * g.tpt, i1 = min(p.ntok, i0 + g.tpt);
+    p.rows[t] = (i1 - i0) * g.G;
+    p.pos[t] = pos0 + i0;
+    int lo = p.key_lo, hi = p.key_hi;
+    p.all_lo[t] = lo;
+    p.all_hi[t] = hi;
+    if (a.causal) {
+      hi = min(hi, pos0 + i1);
+      p.all_hi[t] = min(p.all_hi[t], pos0 + i0 + 1);
+    }
+    if (a.window > 0) {
+      lo = max(lo, pos0 + i0 - a.window + 1);
+      p.all_lo[t] = max(p.all_lo[t], pos0 + i1 - a.window);
+    }
+    if (p.single) {
+      p.first[t] = p.j0 + ((t ^ base) & 1);
+      p.end[t] = p.j1;
+    } else {
+      p.first[t] = hi > lo ? max(p.j0, lo / BN) : p.j0;
+      p.end[t] = hi > lo ? min(p.j1, (hi + BN - 1) / BN) : p.j0;
+    }
+  }
 }
 
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
@@ -238,6 +263,110 @@ template <class T>
 __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_addr, uint32_t accumulate) {
   constexpr uint32_t idesc = idesc_f32acc<T>(BM, D, 0, 1), col_step = 8, v_step = (16 * 128) >> 4;
   mma8_ts<idesc, col_step, v_step>(d_tmem, p_tmem, desc_lo(v_addr, HALF_BYTES), desc_hi(1024), accumulate);
+}
+
+// ceil(a / b) for b > 0, in 32 bits where they serve (a 64-bit division takes about 150
+// instructions, and a launch's first microseconds are one warp's chain of them).
+__device__ __forceinline__ long long div_up(long long a, long long b) {
+  const long long n = a + b - 1;
+  return n <= 0xffffffffLL ? static_cast<long long>(static_cast<unsigned>(n) / static_cast<unsigned>(b)) : n / b;
+}
+// This CTA's run, found by one warp: up to kPlanSeqs sequences, kPlanSeqs / 32 a lane.
+__device__ __forceinline__ void find_run_warp(const ExtendArgs& a, const Geo& g, Ctl& sm, int lane) {
+  constexpr int R = kPlanSeqs / 32;
+  Seq s[R];
+  long long units[R], total = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    s[i] = Seq{0, 0, 0};
+    if (lane + 32 * i < a.B) s[i] = seq_of(a, lane + 32 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    units[i] = 0;
+    if (32 * i < a.B) units[i] = head_units(a, g, s[i], lane);
+    total += units[i];
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+  total *= a.Hkv;
+  const long long length = max(div_up(total, gridDim.x), static_cast<long long>(kMinUnits));
+  const long long begin = blockIdx.x * length, end = min(total, begin + length);
+  if (lane == 0) {
+    sm.run.begin = begin;
+    sm.run.end = end;
+    sm.run.length = length;
+  }
+  long long before = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (32 * i >= a.B || before > begin) break;
+    const long long cost = units[i] * a.Hkv;
+    long long inc = cost;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, x);
+      if (lane >= x) inc += o;
+    }
+    if (before + inc - cost <= begin && begin < before + inc) {
+      sm.run.before = before + inc - cost;
+      sm.run.per_head = units[i];
+      sm.run.b = lane + 32 * i;
+      sm.run.seq = s[i];
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  __syncwarp();
+}
+// The same by the whole block, for more sequences: a thread each, walked in chunks, twice.
+__device__ __noinline__ void find_run_block(const ExtendArgs& a, Ctl& sm, int warp, int lane) {
+  const Geo g{a.Hq / a.Hkv, BM / (a.Hq / a.Hkv)};
+  auto load = [&](int c, Seq& s) {
+    s = Seq{0, 0, 0};
+    if (c + static_cast<int>(threadIdx.x) < a.B) s = seq_of(a, c + threadIdx.x);
+    return head_units(a, g, s, lane);
+  };
+  Seq s;
+  long long total = 0;
+  for (int c = 0; c < a.B; c += NUM_THREADS) total += load(c, s);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+  if (lane == 0) sm.scan[warp] = total;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < WARPS; ++w) total += sm.scan[w];
+  total *= a.Hkv;
+  const long long length = max(div_up(total, gridDim.x), static_cast<long long>(kMinUnits));
+  const long long begin = blockIdx.x * length, end = min(total, begin + length);
+  if (threadIdx.x == 0) {
+    sm.run.begin = begin;
+    sm.run.end = end;
+    sm.run.length = length;
+  }
+  long long before = 0;  // units of the chunks already walked
+  for (int c = 0; c < a.B && before <= begin; c += NUM_THREADS) {
+    const long long units = load(c, s), cost = units * a.Hkv;
+    long long inc = cost;  // inclusive scan over the block
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, x);
+      if (lane >= x) inc += o;
+    }
+    __syncthreads();
+    if (lane == 31) sm.scan[warp] = inc;
+    __syncthreads();
+    long long prior = before;
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) prior += sm.scan[w];
+      before += sm.scan[w];
+    }
+    if (prior + inc - cost <= begin && begin < prior + inc) {
+      sm.run.before = prior + inc - cost;
+      sm.run.per_head = units;
+      sm.run.b = c + threadIdx.x;
+      sm.run.seq = s;
+    }
+  }
 }
 
 #define FA_TMEM_LD16(taddr, r)                                                                       \
@@ -324,33 +453,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int wg = warp >> 2;
-  const Geo geo0{args.Hq / args.Hkv, BM / (args.Hq / args.Hkv)};
-
+  {
+    // One barrier a thread.
+    uint64_t* bars = sm.q_full;
+    constexpr int n1 = (offsetof(Ctl, p_full) - offsetof(Ctl, q_full)) / 8, n2 = (offsetof(Ctl, piece_empty) - offsetof(Ctl, q_full)) / 8;
+    if (threadIdx.x < n2 + NP) {
+      mbar_init(smem_u32(bars + threadIdx.x), threadIdx.x < n1 ? 1 : threadIdx.x < n2 ? WG_THREADS : kPieceReaders);
+      fence_barrier_init();
+    }
+  }
   if (threadIdx.x == 0) {
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&sm.q_full[t]), 1);
-      mbar_init(smem_u32(&sm.q_empty[t]), 1);
-      mbar_init(smem_u32(&sm.s_full[t]), 1);
-      mbar_init(smem_u32(&sm.p_full[t]), WG_THREADS);
-      mbar_init(smem_u32(&sm.o_full[t]), 1);
-      mbar_init(smem_u32(&sm.o_free[t]), WG_THREADS);
-      mbar_init(smem_u32(&sm.st_full[t]), WG_THREADS);
-      mbar_init(smem_u32(&sm.st_empty[t]), WG_THREADS);
-    }
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_u32(&sm.k_full[s]), 1);
-      mbar_init(smem_u32(&sm.k_empty[s]), 1);
-      mbar_init(smem_u32(&sm.v_full[s]), 1);
-      mbar_init(smem_u32(&sm.v_empty[s]), 1);
-    }
-    for (int s = 0; s < NP; ++s) {
-      mbar_init(smem_u32(&sm.piece_full[s]), 1);
-      mbar_init(smem_u32(&sm.piece_empty[s]), kPieceReaders);
-    }
-    mbar_init(smem_u32(&sm.mma_done), 1);
     sm.abort_flag = 0;
-    sm.geo = geo0;
-    fence_barrier_init();
+    const int G = args.Hq / args.Hkv;
+    sm.geo = Geo{G, BM / G};
   }
   if (warp == MMA_WARP) {
     tmem_alloc(smem_u32(&sm.tmem_base), 512);
@@ -361,65 +476,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-
-  // ------------------------------------------------------------ this CTA's run of units
-  // Total units, then the sequence in which the run starts.  Up to NUM_THREADS sequences
-  // are held one to a thread; more are walked in chunks, twice.
-  long long total = 0, mine = 0;
-  long long mine_units = 0;
-  for (int c = 0; c < args.B; c += NUM_THREADS) {
-    Seq s{0, 0, 0};
-    if (c + static_cast<int>(threadIdx.x) < args.B) s = seq_of(args, c + threadIdx.x);
-    const long long u = head_units(args, geo0, s, lane);
-    mine_units = u;
-    mine = u * args.Hkv;
-    total += mine;
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
-  if (lane == 0) sm.scan[warp] = total;
-  if (threadIdx.x == 0) sm.start_b = -1;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) total += sm.scan[w];
-  const long long run = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(kMinUnits));
-  const long long u_begin = blockIdx.x * run, u_end = min(total, u_begin + run);
-  if (u_begin < u_end) {
-    long long before = 0;  // units of the chunks already walked
-    for (int c = 0; c < args.B; c += NUM_THREADS) {
-      if (args.B > NUM_THREADS) {
-        Seq s{0, 0, 0};
-        if (c + static_cast<int>(threadIdx.x) < args.B) s = seq_of(args, c + threadIdx.x);
-        const long long u = head_units(args, geo0, s, lane);
-        mine_units = u;
-        mine = u * args.Hkv;
-      }
-      long long inc = mine;  // inclusive scan over the block
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, inc, x);
-        if (lane >= x) inc += o;
-      }
-      __syncthreads();
-      if (lane == 31) sm.scan[warp] = inc;
-      __syncthreads();
-      long long prior = before, chunk = 0;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) prior += sm.scan[w];
-        chunk += sm.scan[w];
-      }
-      const long long end = prior + inc, first = end - mine;
-      if (first <= u_begin && u_begin < end) {
-        sm.start_b = c + threadIdx.x;
-        sm.start_unit = first;
-        sm.start_units = mine_units;
-      }
-      before += chunk;
-      if (before > u_begin) break;
-    }
-  }
+  // Everything before this overlaps the end of the kernel ahead in the stream.
+  wait_for_previous_kernel();
+  let_next_kernel_start();
+  if (args.B > kPlanSeqs) find_run_block(args, sm, warp, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -435,29 +495,66 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     regs_dec<kOtherRegs>();
     if (warp == PLAN_WARP) {
       // ---------------------------------------------------------- planner
-      // Walks the run item by item and hands out its pieces.
+      // Finds the run, walks it item by item, hands out its pieces and loads their Q tiles.
       const Geo geo = geometry();
+      const uint32_t tiles = tiles_base();
+      if (args.B <= kPlanSeqs) find_run_warp(args, geo, sm, lane);
       ExtendDesc open{0, 0, 0, -1};  // the item that begins here and ends in another CTA
-      int ip = 0;                    // pieces handed out
-      auto hand_out = [&](const Piece& p) {
-        const int s = ip % NP;
-        if (ip >= NP && !mbar_wait_warp(smem_u32(&sm.piece_empty[s]), ((ip / NP) - 1) & 1, abort_flag)) return false;
-        if (lane == 0) {
-          sm.piece[s] = p;
-          mbar_arrive(smem_u32(&sm.piece_full[s]));
-        }
-        __syncwarp();
-        ++ip;
-        return true;
-      };
+      int ip = 0, base = 0;          // pieces handed out, their key tiles
+      int iq = 0, np = 0;            // pieces whose Q is on its way, those of them with keys
+      int nq0 = 0, nq1 = 0;          // Q tiles loaded, per slot
       bool ok = true;
-      if (u_begin < u_end && sm.start_b >= 0) {
-        int b = sm.start_b;
-        Seq s = seq_of(args, b);
-        const long long into = u_begin - sm.start_unit;
-        int h = static_cast<int>(into / sm.start_units);
+      // A one-tile item uses one Q slot, in turn with the next one's, so that its Q tile is
+      // there before the last item is done with its own.
+      auto load_q = [&]() {
+        const Piece& p = pieces.at(iq++);
+        if (p.j0 == p.j1) return;
+        for (int t = 0; t < (p.single ? 1 : 2); ++t) {
+          if (!p.single && !p.any(t)) continue;
+          const int qs = p.single ? np & 1 : t;
+          const int used = qs ? nq1++ : nq0++;
+          if (used > 0) ok = ok && mbar_wait_warp(smem_u32(&sm.q_empty[qs]), (used - 1) & 1, abort_flag);
+          if (!ok) return;
+          if (lane == 0) {
+            const int tokens = p.rows[t] / geo.G;
+            const int boxes = (tokens + q_box_tokens - 1) / q_box_tokens;
+            const uint32_t bar = smem_u32(&sm.q_full[qs]);
+            const int box_rows = q_box_tokens * geo.G;
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * box_rows * 256));
+            for (int i = 0; i < boxes; ++i) {
+              const uint32_t dst = tiles + qs * TILE_BYTES + i * box_rows * 128;
+              const int tok = p.tok0 + t * geo.tpt + i * q_box_tokens;
+              tma_load_3d(dst, &tm_q, bar, 0, p.kvh * geo.G, tok);
+              tma_load_3d(dst + HALF_BYTES, &tm_q, bar, 64, p.kvh * geo.G, tok);
+            }
+          }
+          __syncwarp();
+        }
+        ++np;
+      };
+      // The next place in the ring, once it is free (Q follows at most two pieces behind).
+      auto place = [&]() {
+        while (ok && ip - iq > 2) load_q();
+        if (ok && ip >= NP) ok = mbar_wait_warp(smem_u32(&sm.piece_empty[ip % NP]), ((ip / NP) - 1) & 1, abort_flag);
+        return ok;
+      };
+      // The piece that lane 0 has written there goes out.
+      auto hand_out = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.piece_full[ip % NP]));
+        ++ip;
+      };
+      const long long u_begin = sm.run.begin, u_end = sm.run.end, run = sm.run.length;
+      if (u_begin < u_end) {
+        int b = sm.run.b;
+        Seq s = sm.run.seq;
+        const long long into = u_begin - sm.run.before, per_head = sm.run.per_head;
+        // 32-bit division where it serves: a 64-bit one takes about 150 instructions.
+        int h = into < per_head ? 0
+                : into <= 0xffffffffLL ? static_cast<int>(static_cast<unsigned>(into) / static_cast<unsigned>(per_head))
+                                       : static_cast<int>(into / per_head);
         // The item of key head h in which the run starts, 32 items at a time.
-        long long rem = into % sm.start_units;
+        long long rem = into - h * per_head;
         int p = 0, lo, hi;
         for (const int np = items_of(geo, s.nq); p < np; p += 32) {
           int inc = p + lane < np ? item_units(args, geo, s, p + lane) : 0;
@@ -488,22 +585,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           };
           const int k0 = u_begin <= t0 ? 0 : tile_at(u_begin), k1 = u_end <= t0 ? 0 : tile_at(u_end);
           if (k0 < k1 || (nt == 0 && u0 >= u_begin)) {
-            Piece out;
-            const int i0 = p * 2 * geo.tpt;
-            out.tok0 = s.tok0 + i0;
-            out.ntok = min(s.nq - i0, 2 * geo.tpt);
-            out.pos0 = s.n - s.nq + i0;
-            out.kvh = h;
-            out.b = b;
-            out.j0 = nt ? lo / BN + k0 : 0;
-            out.j1 = nt ? lo / BN + k1 : 0;
-            out.key_lo = lo;
-            out.key_hi = hi;
-            out.slot = k0 == 0 && k1 == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (k0 == 0 ? 1 : 0);
-            out.stop = 0;
-            out.pad = 0;
-            if (k0 == 0 && k1 < nt) open = ExtendDesc{out.tok0, out.ntok, h, static_cast<int>((t0 + static_cast<long long>(nt - 1) * c.tile) / run)};
-            ok = hand_out(out);
+            if (!place()) break;
+            if (lane == 0) {
+              Piece& out = sm.piece[ip % NP];
+              const int i0 = p * 2 * geo.tpt;
+              out.tok0 = s.tok0 + i0;
+              out.ntok = min(s.nq - i0, 2 * geo.tpt);
+              out.kvh = h;
+              out.b = b;
+              out.j0 = nt ? lo / BN + k0 : 0;
+              out.j1 = nt ? lo / BN + k1 : 0;
+              out.key_lo = lo;
+              out.key_hi = hi;
+              out.slot = k0 == 0 && k1 == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (k0 == 0 ? 1 : 0);
+              out.stop = 0;
+              fill_slots(args, geo, out, s.n - s.nq + i0, base);
+              if (k0 == 0 && k1 < nt) {
+                const long long end_unit = t0 + static_cast<long long>(nt - 1) * c.tile;
+                open = ExtendDesc{out.tok0, out.ntok, h, static_cast<int>(div_up(end_unit + 1, run) - 1)};
+              }
+            }
+            hand_out();
+            base += k1 - k0;
           }
           u0 = t0 + nt * c.tile;
           if (++p >= items_of(geo, s.nq)) {
@@ -519,18 +622,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       }
-      if (ok) {
-        Piece w{};
-        w.stop = 1;
-        hand_out(w);
+      if (place()) {
+        if (lane == 0) sm.piece[ip % NP].stop = 1;
+        hand_out();
+        while (ok && iq < ip - 1) load_q();
       }
       if (lane == 0) args.desc[blockIdx.x] = open;
+      if (nq0 > 0) mbar_wait_drain(smem_u32(&sm.q_full[0]), (nq0 - 1) & 1);
+      if (nq1 > 0) mbar_wait_drain(smem_u32(&sm.q_full[1]), (nq1 - 1) & 1);
     } else if (warp == K_WARP || warp == V_WARP) {
-      // ---------------------------------------------------------- K and Q, V producers
+      // ---------------------------------------------------------- K, V producers
       // A warp each, so that K tiles run ahead of the V tiles that wait for a softmax.
       // Lane l holds the tile's block-table entries l, l + 32, ..., fetched one tile ahead
       // (across items too); the boxes go out one after another from one elected lane.
-      const Geo geo = geometry();
       const uint32_t tiles = tiles_base();
       const bool is_k = warp == K_WARP;
       const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
@@ -548,36 +652,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         return wanted(w, j, blk) ? args.block_table[static_cast<long long>(w.b) * args.max_blocks + ((j * BN + blk * rows) >> args.block_shift)] : 0;
       };
       int n = 0;           // tiles loaded so far
-      int np = 0;          // K: items started
-      int nq0 = 0, nq1 = 0;  // K: Q tiles loaded, per slot
       bool ok = true;
-      // The Q tiles of a new item.  A one-tile item uses one slot, in turn with the next
-      // one's, so that its Q tile is there before the last item is done with its own.
-      auto load_q = [&](const Piece& p) {
-        const bool single = one_tile(geo, p);
-        for (int t = 0; t < (single ? 1 : 2); ++t) {
-          if (!single && !slot_tiles(args, geo, p, t, 0).any()) continue;
-          const int qs = single ? np & 1 : t;
-          const int used = qs ? nq1++ : nq0++;
-          if (used > 0) ok = ok && mbar_wait_warp(smem_u32(&sm.q_empty[qs]), (used - 1) & 1, abort_flag);
-          if (!ok) return;
-          if (lane == 0) {
-            const int tokens = min(p.ntok - t * geo.tpt, geo.tpt);
-            const int boxes = (tokens + q_box_tokens - 1) / q_box_tokens;
-            const uint32_t bar = smem_u32(&sm.q_full[qs]);
-            const int box_rows = q_box_tokens * geo.G;
-            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * box_rows * 256));
-            for (int i = 0; i < boxes; ++i) {
-              const uint32_t dst = tiles + qs * TILE_BYTES + i * box_rows * 128;
-              const int tok = p.tok0 + t * geo.tpt + i * q_box_tokens;
-              tma_load_3d(dst, &tm_q, bar, 0, p.kvh * geo.G, tok);
-              tma_load_3d(dst + HALF_BYTES, &tm_q, bar, 64, p.kvh * geo.G, tok);
-            }
-          }
-          __syncwarp();
-        }
-        ++np;
-      };
       // Loads tile j; `id`: this lane's entry of the tile's first 32 blocks (the rest, of
       // blocks of one or two keys, is looked up here).
       auto load_tile = [&](const Piece& p, int j, int id) {
@@ -640,7 +715,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (in >= 0) jn = pieces.at(in).j0;
         }
         if (in >= 0) next = lookup(pieces.at(in), jn, lane);
-        if (is_k && j == pieces.at(ip).j0) load_q(pieces.at(ip));
         if (ok) load_tile(pieces.at(ip), j, cur);
         if (in != ip) pieces.release(ip, lane);
         ip = in;
@@ -651,14 +725,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (ok && ip >= 0) step(odd, even);
       }
       for (int i = max(0, n - NS); i < n; ++i) mbar_wait_drain(smem_u32(&full[i % NS]), (i / NS) & 1);
-      if (nq0 > 0) mbar_wait_drain(smem_u32(&sm.q_full[0]), (nq0 - 1) & 1);
-      if (nq1 > 0) mbar_wait_drain(smem_u32(&sm.q_full[1]), (nq1 - 1) & 1);
     } else {
       // ---------------------------------------------------------- MMA issuer
       // The whole warp runs this (warp-uniform waits); MMAs and commits go out from one
       // elected lane.  Phase bits, bit t for slot t: Q_PH q_full, P_PH p_full and O_PH
       // o_free to wait for next; O_USED: an item has used O_t.
-      const Geo geo = geometry();
       const uint32_t tiles = tiles_base(), tmem = tmem_base();
       enum : uint32_t { Q_PH = 0, P_PH = 2, O_PH = 4, O_USED = 6 };
       uint32_t ph = 0;
@@ -708,12 +779,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // V of tile j of piece p (number g) has landed.  Rows without a key of the item are kept
       // out of the product: whole steps of 16 keys are not issued (`steps`: first and end),
       // the others' rows, and those of blocks outside the pool, are cleared.
-      auto ready_v = [&](const Piece& p, int j, int g, int2& steps) {
+      auto ready_v = [&](const Piece& p, int j, int g, bool edge, int2& steps) {
         if (!mbar_wait_warp(smem_u32(&sm.v_full[g % NS]), static_cast<uint32_t>((g / NS) & 1), abort_flag)) return false;
+        steps = make_int2(0, BN / 16);
         const uint4 bad = *reinterpret_cast<const uint4*>(sm.bad[g & 3]);
+        const bool any_bad = (bad.x | bad.y | bad.z | bad.w) != 0u;
+        if (!edge && !any_bad) return true;
         const int lo = max(0, p.key_lo - j * BN), hi = min(BN, p.key_hi - j * BN);
         steps = make_int2(lo >> 4, (hi + 15) >> 4);
-        const bool any_bad = (bad.x | bad.y | bad.z | bad.w) != 0u;
         if ((lo & 15) != 0 || (hi & 15) != 0 || any_bad) {
           const uint32_t v = tiles + kVOff + g % NS * TILE_BYTES;
           zero_v_rows(v, lo & ~15, lo, lane);
@@ -734,7 +807,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!pieces.wait(is)) return false;
           const Piece& p = pieces.at(is);
           if (p.j0 < p.j1) {
-            if (!one_tile(geo, p)) return false;  // two-tile items issue their own
+            if (!p.single) return false;  // two-tile items issue their own
             s_open = true;
             sj = p.j0;
           } else {
@@ -759,34 +832,36 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int ip = 0; ok && pieces.wait(ip); pieces.release(ip++, lane)) {
         const Piece& p = pieces.at(ip);
         if (p.j0 == p.j1) continue;
-        if (one_tile(geo, p)) {
+        if (p.single) {
           for (int j = p.j0; ok && j < p.j1; ++j, ++g) {
             while (gs < g + 2 && advance_s()) {
             }
             int2 steps;
-            ok = ok && ready_v(p, j, g, steps) && issue_o(g & 1, g, steps, j < p.j0 + 2, j + 2 >= p.j1);
+            ok = ok && ready_v(p, j, g, j == p.j0 || j + 1 == p.j1, steps) &&
+                 issue_o(g & 1, g, steps, j < p.j0 + 2, j + 2 >= p.j1);
             if (ok) free_v(g);
           }
         } else {
           // Two row tiles, a slot each: PV_0, next S_0, PV_1, next S_1.
-          const Tiles t0 = slot_tiles(args, geo, p, 0, 0), t1 = slot_tiles(args, geo, p, 1, 0);
-          const int j1 = p.j1;
+          const int a0 = p.first[0], b0 = p.end[0], a1 = p.first[1], b1 = p.end[1], j1 = p.j1;
+          auto in0 = [&](int k) { return k >= a0 && k < b0; };
+          auto in1 = [&](int k) { return k >= a1 && k < b1; };
           int j = p.j0;
           ok = wait_k(g);
-          if (ok && t0.has(j)) ok = issue_s(0, 0, g, true, j == t0.end - 1);
-          if (ok && t1.has(j)) ok = issue_s(1, 1, g, true, j == t1.end - 1);
+          if (ok && in0(j)) ok = issue_s(0, 0, g, true, j == b0 - 1);
+          if (ok && in1(j)) ok = issue_s(1, 1, g, true, j == b1 - 1);
           if (ok) free_k(g);
           for (; ok && j < j1; ++j, ++g) {
             const bool next = j + 1 < j1;
             int2 steps;
-            ok = ready_v(p, j, g, steps) && (!next || wait_k(g + 1));
-            if (ok && t0.has(j)) ok = issue_o(0, g, steps, j == t0.first, j == t0.end - 1);
-            if (ok && next && t0.has(j + 1)) ok = issue_s(0, 0, g + 1, j + 1 == t0.first, j + 1 == t0.end - 1);
-            if (ok && t1.has(j)) ok = issue_o(1, g, steps, j == t1.first, j == t1.end - 1);
+            ok = ready_v(p, j, g, j == p.j0 || !next, steps) && (!next || wait_k(g + 1));
+            if (ok && in0(j)) ok = issue_o(0, g, steps, j == a0, j == b0 - 1);
+            if (ok && next && in0(j + 1)) ok = issue_s(0, 0, g + 1, j + 1 == a0, j + 1 == b0 - 1);
+            if (ok && in1(j)) ok = issue_o(1, g, steps, j == a1, j == b1 - 1);
             if (!ok) break;
             free_v(g);
             if (next) {
-              if (t1.has(j + 1)) ok = issue_s(1, 1, g + 1, j + 1 == t1.first, j + 1 == t1.end - 1);
+              if (in1(j + 1)) ok = issue_s(1, 1, g + 1, j + 1 == a1, j + 1 == b1 - 1);
               if (ok) free_k(g + 1);
             }
           }
@@ -809,6 +884,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
     const Geo geo = geometry();
+    const int row_tok = row / geo.G;
     const uint32_t tmem = tmem_base();
     const uint32_t stage = tiles_base() + kStageOff + wq * kStageBytes;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
@@ -817,24 +893,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     for (int ip = 0; ok && pieces.wait(ip); pieces.release(ip++, lane)) {
       const Piece& p = pieces.at(ip);
-      const bool single = one_tile(geo, p);
       const int slot = p.slot;
-      for (int rt = 0; rt < (single ? 1 : 2) && ok; ++rt) {
-        const int t = single ? base & 1 : rt;  // the slot; a one-tile item's first
-        const int nrows = tile_rows(geo, p, rt);
-        const bool both = single && p.j1 - p.j0 > 1;
+      for (int rt = 0; rt < (p.single ? 1 : 2) && ok; ++rt) {
+        // t: the slot; of a one-tile item's two, the one whose last tile comes last.
+        const int nt = p.j1 - p.j0;
+        const int t = p.single ? (base + nt - 1) & 1 : rt;
+        const bool both = p.single && nt > 1;
+        const int mine = p.rows[rt] - wq * 32;  // rows of this warp's 32 that hold a token, if positive
         // This row's place in the output or, for a piece, in the workspace.
         long long at;
         if (slot < 0) {
-          const int tok = row / geo.G;
-          at = static_cast<long long>(p.tok0 + rt * geo.tpt + tok) * args.Hq + p.kvh * geo.G + row - tok * geo.G;
+          at = static_cast<long long>(p.tok0 + rt * geo.tpt + row_tok) * args.Hq + p.kvh * geo.G + row - row_tok * geo.G;
         } else {
           at = static_cast<long long>(slot) * args.slot_rows + rt * BM + row;
         }
         float* lse = slot < 0 ? args.lse : args.ws_lse;
-        if (!slot_tiles(args, geo, p, t, base).any()) {
+        if (nt == 0 || !p.any(t)) {
           // No key tile: a whole item's rows see nothing; a piece adds nothing.
-          if (row < nrows) {
+          if (lane < mine) {
             if (lse != nullptr) lse[at] = -INFINITY;
             if (slot < 0) {
               uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.o) + at * D);
@@ -844,18 +920,49 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           continue;
         }
-        for (int i = 0; ok && i < (both ? 2 : 1); ++i)
-          ok = mbar_wait_warp(smem_u32(&sm.o_full[t ^ i]), ph >> (t ^ i) & 1u, abort_flag) &&
-               mbar_wait_warp(smem_u32(&sm.st_full[t ^ i]), ph >> (t ^ i) & 1u, abort_flag);
+        float m1 = -INFINITY, l1 = 0.f;
+        bool staged = false;
+        if (both) {
+          // The other slot is done one tile earlier.  With a few rows its O is put aside in the
+          // stage, so that the next item's first tile finds the slot free.
+          ok = mbar_wait_warp(smem_u32(&sm.o_full[t ^ 1]), ph >> (t ^ 1) & 1u, abort_flag) &&
+               mbar_wait_warp(smem_u32(&sm.st_full[t ^ 1]), ph >> (t ^ 1) & 1u, abort_flag);
+          if (!ok) break;
+          ph ^= 1u << (t ^ 1);
+          tc_fence_after();
+          m1 = sm.stat_m[t ^ 1][row];
+          l1 = sm.stat_l[t ^ 1][row];
+          mbar_arrive(smem_u32(&sm.st_empty[t ^ 1]));
+          staged = p.rows[0] <= kDirectRows;
+          if (staged) {
+            if (mine > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t r[32];
+                FA_TMEM_LD32(tmem + lane_off + 256 + (t ^ 1) * 128 + c, r);
+                tmem_ld_wait();
+                if (lane < mine) {
+#pragma unroll
+                  for (int v = 0; v < 8; ++v)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * (D * 4) + c * 4 + v * 16),
+                                 "r"(r[4 * v]), "r"(r[4 * v + 1]), "r"(r[4 * v + 2]), "r"(r[4 * v + 3])
+                                 : "memory");
+                }
+              }
+            }
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sm.o_free[t ^ 1]));
+          }
+        }
+        ok = mbar_wait_warp(smem_u32(&sm.o_full[t]), ph >> t & 1u, abort_flag) &&
+             mbar_wait_warp(smem_u32(&sm.st_full[t]), ph >> t & 1u, abort_flag);
         if (!ok) break;
-        ph ^= both ? 3u : 1u << t;
+        ph ^= 1u << t;
         tc_fence_after();
         float m = sm.stat_m[t][row], l = sm.stat_l[t][row];
         mbar_arrive(smem_u32(&sm.st_empty[t]));
         float f0 = 1.f, f1 = 0.f;
         if (both) {
-          const float m1 = sm.stat_m[t ^ 1][row], l1 = sm.stat_l[t ^ 1][row];
-          mbar_arrive(smem_u32(&sm.st_empty[t ^ 1]));
           const float mm = fmaxf(m, m1);
           f0 = m == -INFINITY ? 0.f : ex2_approx((m - mm) * args.scale_log2);
           f1 = m1 == -INFINITY ? 0.f : ex2_approx((m1 - mm) * args.scale_log2);
@@ -864,7 +971,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         // l > 0: the row saw keys; l = 0: none; NaN marks a NaN score.
         const bool none = l == 0.f;
-        if (row < nrows && lse != nullptr) lse[at] = l > 0.f ? m * args.scale + logf(l) : (none ? -INFINITY : l);
+        if (lane < mine && lse != nullptr) lse[at] = l > 0.f ? m * args.scale + logf(l) : (none ? -INFINITY : l);
         const float inv = l > 0.f ? 1.f / l : (none ? 0.f : l);
         f0 *= inv;
         f1 *= inv;
@@ -873,15 +980,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool part = slot >= 0;
         char* out = part ? reinterpret_cast<char*>(args.ws_o) : static_cast<char*>(args.o);
         at *= part ? D * 4 : D * 2;  // bytes from here on
-        const int mine = nrows - wq * 32;  // rows of this warp's 32 that hold a token
         if (mine > 0 && mine <= kDirectRows) {
           // A few rows: each lane writes its own.
           char* dst = out + at;
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             float o[16];
-            load_o16(tO + c, tO1 + c, both, none, f0, f1, o);
-            if (row < nrows) {
+            load_o16(tO + c, tO1 + c, both && !staged, none, f0, f1, o);
+            if (lane < mine) {
+              if (staged && !none) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                  float4 x;
+                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                               : "r"(stage + lane * (D * 4) + c * 4 + v * 16));
+                  o[4 * v] = fmaf(x.x, f1, o[4 * v]);
+                  o[4 * v + 1] = fmaf(x.y, f1, o[4 * v + 1]);
+                  o[4 * v + 2] = fmaf(x.z, f1, o[4 * v + 2]);
+                  o[4 * v + 3] = fmaf(x.w, f1, o[4 * v + 3]);
+                }
+              }
               if (part) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
@@ -935,10 +1054,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               at += 128;
             }
           }
+          __syncwarp();  // the stage may be written otherwise next
         }
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.o_free[t]));
-        if (both) mbar_arrive(smem_u32(&sm.o_free[t ^ 1]));
+        if (both && !staged) mbar_arrive(smem_u32(&sm.o_free[t ^ 1]));
       }
       base += p.j1 - p.j0;
     }
@@ -947,11 +1067,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // Warpgroup t is the softmax of slot t: thread = row, all 128 score columns of a key
     // tile in registers (as in fwd_tc.cu).  A warp without a valid row only keeps step.
     regs_inc<kSoftmaxRegs>();
-    const Geo geo = geometry();
     const uint32_t tmem = tmem_base();
     const int t = wg;
     const int wq = warp & 3;
-    const int row = wq * 32 + lane;
+    const int row = wq * 32 + lane, row_tok = row / geometry().G;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off + t * 128;
     const uint32_t tO = tS + 256;
@@ -969,26 +1088,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool busy;
       {
         const Piece& p = pieces.at(ip);
-        const Tiles my = slot_tiles(args, geo, p, t, base);
-        j = my.first;
-        end = my.end;
-        step = my.step;
+        j = p.first[t];
+        end = p.end[t];
+        step = p.single ? 2 : 1;
         bad_at = base - p.j0;
         base += p.j1 - p.j0;
-        const int rt = one_tile(geo, p) ? 0 : t;  // the slot's row tile
-        busy = wq * 32 < tile_rows(geo, p, rt);
-        row_lo = all_lo = p.key_lo;
-        row_hi = all_hi = p.key_hi;
-        const int first = p.pos0 + rt * geo.tpt, last = first + min(p.ntok - rt * geo.tpt, geo.tpt) - 1;
-        const int mine = first + row / geo.G;
-        if (args.causal) {
-          row_hi = min(row_hi, mine + 1);
-          all_hi = min(all_hi, first + 1);
-        }
-        if (args.window > 0) {
-          row_lo = max(row_lo, mine - args.window + 1);
-          all_lo = max(all_lo, last - args.window + 1);
-        }
+        busy = wq * 32 < p.rows[t];
+        row_lo = p.key_lo;
+        row_hi = p.key_hi;
+        all_lo = p.all_lo[t];
+        all_hi = p.all_hi[t];
+        const int pos = p.pos[t] + row_tok;
+        if (args.causal) row_hi = min(row_hi, pos + 1);
+        if (args.window > 0) row_lo = max(row_lo, pos - args.window + 1);
         pieces.release(ip, lane);
       }
       if (j >= end) continue;
@@ -1129,6 +1241,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 constexpr int CB_WARPS = 8;
 template <class T>
 __global__ void __launch_bounds__(CB_WARPS * 32) combine_kernel(const __grid_constant__ ExtendArgs args) {
+  wait_for_previous_kernel();
   const ExtendDesc d = args.desc[blockIdx.x];
   if (d.last < 0) return;
   const int lane = threadIdx.x & 31;
@@ -1208,12 +1321,10 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
   e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(sms < kExtendMaxCtas ? sms : kExtendMaxCtas);
-  kernel<<<grid, NUM_THREADS, kSmemBytes, stream>>>(tq, tk, tv, a, box);
-  e = cudaGetLastError();
+  e = launch_dependent(kernel, dim3(grid), dim3(NUM_THREADS), kSmemBytes, stream, tq, tk, tv, a, box);
   if (e != cudaSuccess) return e;
   const dim3 cgrid(grid, (a.slot_rows + CB_WARPS * 4 - 1) / (CB_WARPS * 4));
-  (a.f16 ? combine_kernel<F16> : combine_kernel<Bf16>)<<<cgrid, CB_WARPS * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(a.f16 ? combine_kernel<F16> : combine_kernel<Bf16>, cgrid, dim3(CB_WARPS * 32), 0, stream, a);
 }
 
 cudaError_t take_status_extend(unsigned int* out) { return take_local_status(out); }

@@ -169,17 +169,18 @@ bool make_tmap_3d_half(void* map, const void* base, const long long dims[3], con
 // overlaps that one's end (a few microseconds less between them).  The kernel has to call
 // wait_for_previous_kernel() before it reads what that one writes.
 template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A... args) {
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per device and kernel.
 cudaError_t set_max_dynamic_smem(const void* func, size_t bytes);

@@ -239,7 +239,7 @@ cudaError_t launch(const NormRopeArgs& a, bool backward, cudaStream_t stream) {
       <<<blocks, THREADS, 0, stream>>>(a, static_cast<unsigned>(tiles), blocks_q);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.norm || a.partials == nullptr) return e;
-  return launch_dependent(sum_partials_kernel<E>, dim3(D / 32, gk ? 2 : 1), dim3(1024), stream, a,
+  return launch_dependent(sum_partials_kernel<E>, dim3(D / 32, gk ? 2 : 1), dim3(1024), 0, stream, a,
                           static_cast<int>(blocks_q), static_cast<int>(blocks));
 }
 
