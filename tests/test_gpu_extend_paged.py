@@ -93,6 +93,29 @@ def test_more_sequences_than_threads(B):
     check([1 + (b % 3 == 0) for b in range(B)], [2 + 7 * b % 60 for b in range(B)], 2, 1, 16, seed=B)
 
 
+@pytest.mark.parametrize("B", [40, 300])
+def test_padded_decode_batch(B):
+    """A batch padded with sequences of length zero, one token each, many of them in a row."""
+    total = [0 if 3 < b < B - 2 else 50 + 90 * b for b in range(B)]
+    total = [min(n, 700) for n in total]
+    q, kp, vp, table, cu, lens = make([1] * B, total, 8, 2, 16, BF16, seed=31)
+    o, lse = fa.extend_paged(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), lens.cuda())
+    assert fa.device_status() == fa.FA_OK
+    empty = lens == 0
+    assert (o[empty] == 0).all() and lse[empty].isneginf().all()
+    o_ref, l_ref, ob, lb = attend(q, kp, vp, table, cu, lens)
+    assert_within(o[~empty], o_ref[~empty], ob[~empty], "o")
+    assert_within(lse[~empty], l_ref[~empty], lb[~empty], "lse")
+
+
+@pytest.mark.parametrize("order", [(1, 300, 1), (300, 1, 1, 300, 300, 5), (1, 1, 300, 1, 300)])
+@pytest.mark.parametrize("n", [100, 129, 400, 650])
+def test_one_and_two_tile_items_in_turn(order, n):
+    """Items of one and of two row tiles after one another, with even and odd numbers of key tiles."""
+    check(list(order), [m + n for m in order], 4, 1, 16, seed=n)
+    check(list(order), [m + n for m in order], 4, 2, 64, FP16, seed=n + 1, window=300)
+
+
 def test_long_cache_spread_over_the_whole_grid():
     check([1], [20000], 2, 1, 16, seed=8)
     check([3], [20000], 2, 1, 128, FP16, seed=9)

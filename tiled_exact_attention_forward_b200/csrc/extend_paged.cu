@@ -43,7 +43,6 @@ constexpr int NS = 2;                       // stages of the K ring and of the V
 constexpr int TILE_BYTES = BM * D * 2;
 constexpr int HALF_BYTES = TILE_BYTES / 2;  // one 64-column half (128-byte rows, swizzled)
 constexpr int NUM_THREADS = 512;
-constexpr int WARPS = NUM_THREADS / 32;
 constexpr int WG_THREADS = 128;
 constexpr int EPI_WG = 2;
 constexpr int PLAN_WARP = 12;
@@ -69,16 +68,18 @@ struct Cost {
 };
 constexpr int kItemUnits1 = 4, kTileUnits1 = 2, kItemUnits2 = 7, kTileUnits2 = 3;  // items of one, two row tiles
 constexpr int kMinUnits = 6;
-// Up to so many sequences the planner warp finds the CTA's run alone; for more the whole
-// block does, ahead of everything else.
-constexpr int kPlanSeqs = 128;
+// The planner keeps the units of so many sequences; it works those of more out twice.
+constexpr int kPlanSeqs = 1024;
 // Epilogue: up to so many rows of a warp are written by their own lanes; more go through
 // shared memory, so that a store instruction does not touch 32 lines.
 constexpr int kDirectRows = 8;
 
+// A wait gives up after so many cycles.
+constexpr unsigned kWaitCycles = 2000000000u;
+
 // A run of key tiles [j0, j1) of one item, as the planner hands it to the other warps.
-// Arrays go by slot: a one-tile item's tiles take the slots in turn, through the items
-// (the CTA's tile number g goes to slot g % 2); a two-tile item's row tiles have one each.
+// Arrays go by slot: a one-tile item's key tiles take the slots in turn, going on from the
+// item before; a two-tile item's row tiles have one each.
 struct Piece {
   int j0, j1;
   int single;                  // one row tile
@@ -86,7 +87,9 @@ struct Piece {
   int b, kvh;
   int key_lo, key_hi;          // keys of the sequence that some row of the item sees
   int tok0, ntok;              // the item's tokens in the packed batch
-  int slot;                    // workspace slot of the partial result, -1: the piece is the whole item
+  int part;                    // workspace slot of the partial result, -1: the piece is the whole item
+  int tile0;                   // the CTA's number of key tile j0: its place in the rings
+  int slot0;                   // a one-tile item's slot for key tile j0
   int pad;
   int first[2], end[2];        // key tiles of the slot: first, end; every second one of a one-tile item
   int rows[2];                 // rows of the slot's row tile that hold a token
@@ -117,7 +120,6 @@ struct Run {
   long long begin, end, length;
   long long before, per_head;
   int b;
-  Seq seq;
 };
 
 // Everything else sits in static shared memory, whose addresses are constants: pointers
@@ -136,8 +138,8 @@ struct Ctl {
   uint64_t st_full[2], st_empty[2];
   uint64_t piece_empty[NP];
   float stat_m[2][BM], stat_l[2][BM];
-  long long scan[WARPS];
   Run run;
+  long long units[kPlanSeqs];        // per key head, of each sequence
   Geo geo;
   uint32_t tmem_base;
   int abort_flag;
@@ -186,9 +188,12 @@ __device__ __forceinline__ int items_of(const Geo& g, int nq) { return (nq + 2 *
 __device__ __forceinline__ long long head_units(const ExtendArgs& a, const Geo& g, const Seq& s, int lane) {
   const int np = items_of(g, s.nq);
   long long u = 0;
-  if (np <= 4)
+  if (np <= 4) {
+#pragma unroll 1
     for (int p = 0; p < np; ++p) u += item_units(a, g, s, p);
+  }
   unsigned many = __ballot_sync(0xffffffffu, np > 4);
+#pragma unroll 1
   while (many) {
     const int src = __ffs(many) - 1;
     many &= many - 1;
@@ -196,6 +201,7 @@ __device__ __forceinline__ long long head_units(const ExtendArgs& a, const Geo& 
                 __shfl_sync(0xffffffffu, s.n, src)};
     const int onp = items_of(g, o.nq);
     long long v = 0;
+#pragma unroll 1
     for (int p = lane; p < onp; p += 32) v += item_units(a, g, o, p);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
@@ -204,10 +210,8 @@ __device__ __forceinline__ long long head_units(const ExtendArgs& a, const Geo& 
   return u;
 }
 
-// The piece's fields by slot; `base`: key tiles of the CTA's pieces before it, pos0: the
-// position of its first token.
-__device__ __forceinline__ void fill_slots(const ExtendArgs& a, const Geo& g, Piece& p, int pos0, int base) {
-  p.single = p.ntok <= g.tpt;
+// The piece's fields by slot; pos0: the position of its first token.
+__device__ __forceinline__ void fill_slots(const ExtendArgs& a, const Geo& g, Piece& p, int pos0) {
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int i0 = p.single ? 0 : t * g.tpt, i1 = min(p.ntok, i0 + g.tpt);
@@ -225,7 +229,7 @@ __device__ __forceinline__ void fill_slots(const ExtendArgs& a, const Geo& g, Pi
       p.all_lo[t] = max(p.all_lo[t], pos0 + i1 - a.window);
     }
     if (p.single) {
-      p.first[t] = p.j0 + ((t ^ base) & 1);
+      p.first[t] = p.j0 + (t ^ p.slot0);
       p.end[t] = p.j1;
     } else {
       p.first[t] = hi > lo ? max(p.j0, lo / BN) : p.j0;
@@ -265,108 +269,57 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
   mma8_ts<idesc, col_step, v_step>(d_tmem, p_tmem, desc_lo(v_addr, HALF_BYTES), desc_hi(1024), accumulate);
 }
 
-// ceil(a / b) for b > 0, in 32 bits where they serve (a 64-bit division takes about 150
-// instructions, and a launch's first microseconds are one warp's chain of them).
-__device__ __forceinline__ long long div_up(long long a, long long b) {
-  const long long n = a + b - 1;
-  return n <= 0xffffffffLL ? static_cast<long long>(static_cast<unsigned>(n) / static_cast<unsigned>(b)) : n / b;
+// ceil(a / b) for 0 <= a < 2^48, 0 < b < 2^16, by two 32-bit divisions (a 64-bit one takes
+// about 150 instructions, and a launch's first microseconds are one warp's chain of them).
+__device__ __forceinline__ long long div_up(long long a, unsigned b) {
+  const unsigned hi = static_cast<unsigned>((a + b - 1) >> 16), lo = static_cast<unsigned>(a + b - 1) & 0xffffu;
+  const unsigned q = hi / b;
+  return (static_cast<long long>(q) << 16) + ((hi - q * b) << 16 | lo) / b;
 }
-// This CTA's run, found by one warp: up to kPlanSeqs sequences, kPlanSeqs / 32 a lane.
-__device__ __forceinline__ void find_run_warp(const ExtendArgs& a, const Geo& g, Ctl& sm, int lane) {
-  constexpr int R = kPlanSeqs / 32;
-  Seq s[R];
-  long long units[R], total = 0;
+// This CTA's run, found by one warp, 32 sequences at a time.  The units of the first
+// kPlanSeqs are kept for the second walk.
+__device__ __forceinline__ void find_run(const ExtendArgs& a, const Geo& g, Ctl& sm, int lane) {
+  long long total = 0, length = 0, begin = 0, before = 0;
+#pragma unroll 1
+  for (int walk = 0; walk < 2; ++walk) {
+#pragma unroll 1
+    for (int c = 0; c < a.B && (walk == 0 || before <= begin); c += 32) {
+      long long units;
+      if (walk == 1 && c < kPlanSeqs) {
+        units = sm.units[c + lane];
+      } else {
+        Seq s{0, 0, 0};
+        if (c + lane < a.B) s = seq_of(a, c + lane);
+        units = head_units(a, g, s, lane);
+        if (c < kPlanSeqs) sm.units[c + lane] = units;
+      }
+      const long long cost = units * a.Hkv;
+      long long inc = cost;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    s[i] = Seq{0, 0, 0};
-    if (lane + 32 * i < a.B) s[i] = seq_of(a, lane + 32 * i);
+      for (int x = 1; x < 32; x <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, inc, x);
+        if (lane >= x) inc += o;
+      }
+      if (walk == 1 && before + inc - cost <= begin && begin < before + inc) {
+        sm.run.before = before + inc - cost;
+        sm.run.per_head = units;
+        sm.run.b = c + lane;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (walk == 0) {
+      total = before;
+      before = 0;
+      length = max(div_up(total, gridDim.x), static_cast<long long>(kMinUnits));
+      begin = blockIdx.x * length;
+    }
   }
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    units[i] = 0;
-    if (32 * i < a.B) units[i] = head_units(a, g, s[i], lane);
-    total += units[i];
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
-  total *= a.Hkv;
-  const long long length = max(div_up(total, gridDim.x), static_cast<long long>(kMinUnits));
-  const long long begin = blockIdx.x * length, end = min(total, begin + length);
   if (lane == 0) {
     sm.run.begin = begin;
-    sm.run.end = end;
+    sm.run.end = min(total, begin + length);
     sm.run.length = length;
-  }
-  long long before = 0;
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (32 * i >= a.B || before > begin) break;
-    const long long cost = units[i] * a.Hkv;
-    long long inc = cost;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, inc, x);
-      if (lane >= x) inc += o;
-    }
-    if (before + inc - cost <= begin && begin < before + inc) {
-      sm.run.before = before + inc - cost;
-      sm.run.per_head = units[i];
-      sm.run.b = lane + 32 * i;
-      sm.run.seq = s[i];
-    }
-    before += __shfl_sync(0xffffffffu, inc, 31);
   }
   __syncwarp();
-}
-// The same by the whole block, for more sequences: a thread each, walked in chunks, twice.
-__device__ __noinline__ void find_run_block(const ExtendArgs& a, Ctl& sm, int warp, int lane) {
-  const Geo g{a.Hq / a.Hkv, BM / (a.Hq / a.Hkv)};
-  auto load = [&](int c, Seq& s) {
-    s = Seq{0, 0, 0};
-    if (c + static_cast<int>(threadIdx.x) < a.B) s = seq_of(a, c + threadIdx.x);
-    return head_units(a, g, s, lane);
-  };
-  Seq s;
-  long long total = 0;
-  for (int c = 0; c < a.B; c += NUM_THREADS) total += load(c, s);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
-  if (lane == 0) sm.scan[warp] = total;
-  __syncthreads();
-  total = 0;
-  for (int w = 0; w < WARPS; ++w) total += sm.scan[w];
-  total *= a.Hkv;
-  const long long length = max(div_up(total, gridDim.x), static_cast<long long>(kMinUnits));
-  const long long begin = blockIdx.x * length, end = min(total, begin + length);
-  if (threadIdx.x == 0) {
-    sm.run.begin = begin;
-    sm.run.end = end;
-    sm.run.length = length;
-  }
-  long long before = 0;  // units of the chunks already walked
-  for (int c = 0; c < a.B && before <= begin; c += NUM_THREADS) {
-    const long long units = load(c, s), cost = units * a.Hkv;
-    long long inc = cost;  // inclusive scan over the block
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, inc, x);
-      if (lane >= x) inc += o;
-    }
-    __syncthreads();
-    if (lane == 31) sm.scan[warp] = inc;
-    __syncthreads();
-    long long prior = before;
-    for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) prior += sm.scan[w];
-      before += sm.scan[w];
-    }
-    if (prior + inc - cost <= begin && begin < prior + inc) {
-      sm.run.before = prior + inc - cost;
-      sm.run.per_head = units;
-      sm.run.b = c + threadIdx.x;
-      sm.run.seq = s;
-    }
-  }
 }
 
 #define FA_TMEM_LD16(taddr, r)                                                                       \
@@ -412,6 +365,24 @@ __device__ __forceinline__ void load_o16(uint32_t tO, uint32_t tO1, bool both, b
   for (int e = 0; e < 16; ++e) o[e] = none ? 0.f : o[e];
 }
 
+// The bounded wait of common.cuh for a whole warp, in fewer instructions: there are some
+// thirty waits here.  (A suspend-time hint on try_wait, to leave the issue slots to the
+// softmax warps, measured 3 % slower.)
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  bool ok = true;
+  const unsigned t0 = static_cast<unsigned>(clock());
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    // About a second at the B200's clocks; the kernel's end reports it.
+    if (*abort_flag || static_cast<unsigned>(clock()) - t0 > kWaitCycles) {
+      *abort_flag = 1;
+      ok = false;
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 // A warp's view of the planner's ring of pieces.  Pieces stay in shared memory until the
 // warp releases them: what a role needs of one now and then is read there, since a
 // spilled register costs a local load, and with this much shared memory in use little
@@ -423,7 +394,7 @@ struct Pieces {
   __device__ __forceinline__ const Piece& at(int i) const { return sm->piece[i % NP]; }
   // Waits for piece i; false at the end (or when the CTA gives up).
   __device__ __forceinline__ bool wait(int i) const {
-    return mbar_wait_warp(smem_u32(&sm->piece_full[i % NP]), (i / NP) & 1, abort_flag) && !at(i).stop;
+    return wait_bar(smem_u32(&sm->piece_full[i % NP]), (i / NP) & 1, abort_flag) && !at(i).stop;
   }
   __device__ __forceinline__ void release(int i, int lane) const {
     __syncwarp();
@@ -440,6 +411,7 @@ __device__ __forceinline__ void zero_v_rows(uint32_t v_addr, int r0, int r1, int
 }
 // Zeroes the rows of blocks outside the pool (bit r of `bad`).
 __device__ __noinline__ void zero_bad_rows(uint32_t v_addr, const uint32_t* bad, int lane) {
+#pragma unroll 1
   for (int r = 0; r < BN; ++r)
     if (bad[r >> 5] >> (r & 31) & 1u) zero_v_rows(v_addr, r, r + 1, lane);
 }
@@ -479,7 +451,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // Everything before this overlaps the end of the kernel ahead in the stream.
   wait_for_previous_kernel();
   let_next_kernel_start();
-  if (args.B > kPlanSeqs) find_run_block(args, sm, warp, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -498,64 +469,70 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // Finds the run, walks it item by item, hands out its pieces and loads their Q tiles.
       const Geo geo = geometry();
       const uint32_t tiles = tiles_base();
-      if (args.B <= kPlanSeqs) find_run_warp(args, geo, sm, lane);
+      find_run(args, geo, sm, lane);
       ExtendDesc open{0, 0, 0, -1};  // the item that begins here and ends in another CTA
-      int ip = 0, base = 0;          // pieces handed out, their key tiles
-      int iq = 0, np = 0;            // pieces whose Q is on its way, those of them with keys
+      int ip = 0, tile0 = 0, slot0 = 0;  // pieces handed out, their key tiles, the next slot in turn
+      int iq = 0;                    // pieces whose Q is on its way
       int nq0 = 0, nq1 = 0;          // Q tiles loaded, per slot
       bool ok = true;
       // A one-tile item uses one Q slot, in turn with the next one's, so that its Q tile is
       // there before the last item is done with its own.
       auto load_q = [&]() {
-        const Piece& p = pieces.at(iq++);
-        if (p.j0 == p.j1) return;
+        const Piece& p = pieces.at(iq);
+#pragma unroll 1
         for (int t = 0; t < (p.single ? 1 : 2); ++t) {
           if (!p.single && !p.any(t)) continue;
-          const int qs = p.single ? np & 1 : t;
+          const int qs = p.single ? iq & 1 : t;
           const int used = qs ? nq1++ : nq0++;
-          if (used > 0) ok = ok && mbar_wait_warp(smem_u32(&sm.q_empty[qs]), (used - 1) & 1, abort_flag);
+          if (used > 0) ok = wait_bar(smem_u32(&sm.q_empty[qs]), (used - 1) & 1, abort_flag);
           if (!ok) return;
           if (lane == 0) {
-            const int tokens = p.rows[t] / geo.G;
-            const int boxes = (tokens + q_box_tokens - 1) / q_box_tokens;
-            const uint32_t bar = smem_u32(&sm.q_full[qs]);
-            const int box_rows = q_box_tokens * geo.G;
-            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * box_rows * 256));
-            for (int i = 0; i < boxes; ++i) {
-              const uint32_t dst = tiles + qs * TILE_BYTES + i * box_rows * 128;
-              const int tok = p.tok0 + t * geo.tpt + i * q_box_tokens;
+            const uint32_t bar = smem_u32(&sm.q_full[qs]), bytes = q_box_tokens * geo.G * 256;
+            uint32_t dst = tiles + qs * TILE_BYTES;
+            const int end = p.tok0 + min(p.ntok, (t + 1) * geo.tpt);
+#pragma unroll 1
+            for (int tok = p.tok0 + t * geo.tpt; tok < end; tok += q_box_tokens, dst += bytes / 2) {
+              mbar_expect_tx(bar, bytes);
               tma_load_3d(dst, &tm_q, bar, 0, p.kvh * geo.G, tok);
               tma_load_3d(dst + HALF_BYTES, &tm_q, bar, 64, p.kvh * geo.G, tok);
             }
+            mbar_arrive(bar);
           }
           __syncwarp();
         }
-        ++np;
-      };
-      // The next place in the ring, once it is free (Q follows at most two pieces behind).
-      auto place = [&]() {
-        while (ok && ip - iq > 2) load_q();
-        if (ok && ip >= NP) ok = mbar_wait_warp(smem_u32(&sm.piece_empty[ip % NP]), ((ip / NP) - 1) & 1, abort_flag);
-        return ok;
-      };
-      // The piece that lane 0 has written there goes out.
-      auto hand_out = [&]() {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.piece_full[ip % NP]));
-        ++ip;
+        ++iq;
       };
       const long long u_begin = sm.run.begin, u_end = sm.run.end, run = sm.run.length;
+      int b = 0, h = 0, p = 0;       // the item: sequence, key head, number
+      Seq s{0, 0, 0};
+      long long u0 = u_end;          // its first unit (an empty run: past the end)
+      auto next_item = [&]() {
+        if (++p * 2 * geo.tpt < s.nq) return;
+        p = 0;
+        if (++h < args.Hkv) return;
+        h = 0;
+        // Sequences without new tokens have no items; the run ends before they run out.
+#pragma unroll 1
+        do {
+          if (++b >= args.B) return;
+          s = seq_of(args, b);
+        } while (s.nq == 0);
+      };
       if (u_begin < u_end) {
-        int b = sm.run.b;
-        Seq s = sm.run.seq;
+        b = sm.run.b;
+        s = seq_of(args, b);
         const long long into = u_begin - sm.run.before, per_head = sm.run.per_head;
-        // 32-bit division where it serves: a 64-bit one takes about 150 instructions.
-        int h = into < per_head ? 0
-                : into <= 0xffffffffLL ? static_cast<int>(static_cast<unsigned>(into) / static_cast<unsigned>(per_head))
-                                       : static_cast<int>(into / per_head);
+        // h = into / per_head, bit by bit where 32-bit division does not serve.
+        if (into <= 0xffffffffLL) {
+          if (into >= per_head) h = static_cast<int>(static_cast<unsigned>(into) / static_cast<unsigned>(per_head));
+        } else {
+#pragma unroll 1
+          for (int bit = 1 << 30; bit > 0; bit >>= 1)
+            if ((h | bit) * per_head <= into) h |= bit;
+        }
         // The item of key head h in which the run starts, 32 items at a time.
         long long rem = into - h * per_head;
-        int p = 0, lo, hi;
+#pragma unroll 1
         for (const int np = items_of(geo, s.nq); p < np; p += 32) {
           int inc = p + lane < np ? item_units(args, geo, s, p + lane) : 0;
           const int own = inc;
@@ -573,60 +550,89 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           rem -= __shfl_sync(0xffffffffu, inc, 31);
         }
-        long long u0 = u_begin - rem;  // the item's first unit
-        while (ok && u0 < u_end) {
-          const int nt = item_tiles(args, geo, s, p, lo, hi);
-          // Tile k of the item begins at unit u0 + c.item + k c.tile, and the run that holds
-          // this unit takes it; unit u0 only says who writes an item without keys.
-          const Cost c = cost_of(geo, s, p);
+        u0 = u_begin - rem;
+      }
+      // One turn: the next piece of the run, or the end, goes out.
+#pragma unroll 1
+      for (bool stop = false; ok && !stop;) {
+        int nt = 0, lo = 0, hi = 0, k0 = 0, k1 = 0;
+        Cost c{0, 0};
+        // To the next item with a key tile in the run.
+#pragma unroll 1
+        while (true) {
+          stop = u0 >= u_end;
+          if (stop) break;
+          nt = item_tiles(args, geo, s, p, lo, hi);
+          c = cost_of(geo, s, p);
+          // Tile k of the item begins at unit t0 + k c.tile, and the run that holds this unit
+          // takes it; unit u0 only says who writes an item without keys.
           const long long t0 = u0 + c.item;
           auto tile_at = [&](long long u) {
-            return static_cast<int>(min(max((u - t0 + c.tile - 1) / c.tile, 0LL), static_cast<long long>(nt)));
+            const int x = static_cast<int>(min(max(u - t0, 0LL), static_cast<long long>(nt * c.tile)));
+            return c.tile == kTileUnits1 ? (x + kTileUnits1 - 1) / kTileUnits1 : (x + kTileUnits2 - 1) / kTileUnits2;
           };
-          const int k0 = u_begin <= t0 ? 0 : tile_at(u_begin), k1 = u_end <= t0 ? 0 : tile_at(u_end);
-          if (k0 < k1 || (nt == 0 && u0 >= u_begin)) {
-            if (!place()) break;
-            if (lane == 0) {
-              Piece& out = sm.piece[ip % NP];
-              const int i0 = p * 2 * geo.tpt;
-              out.tok0 = s.tok0 + i0;
-              out.ntok = min(s.nq - i0, 2 * geo.tpt);
-              out.kvh = h;
-              out.b = b;
-              out.j0 = nt ? lo / BN + k0 : 0;
-              out.j1 = nt ? lo / BN + k1 : 0;
-              out.key_lo = lo;
-              out.key_hi = hi;
-              out.slot = k0 == 0 && k1 == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (k0 == 0 ? 1 : 0);
-              out.stop = 0;
-              fill_slots(args, geo, out, s.n - s.nq + i0, base);
-              if (k0 == 0 && k1 < nt) {
-                const long long end_unit = t0 + static_cast<long long>(nt - 1) * c.tile;
-                open = ExtendDesc{out.tok0, out.ntok, h, static_cast<int>(div_up(end_unit + 1, run) - 1)};
-              }
-            }
-            hand_out();
-            base += k1 - k0;
-          }
-          u0 = t0 + nt * c.tile;
-          if (++p >= items_of(geo, s.nq)) {
-            p = 0;
-            if (++h >= args.Hkv) {
-              h = 0;
-              do {
-                if (++b >= args.B) break;
-                s = seq_of(args, b);
-              } while (s.nq == 0);
-              if (b >= args.B) break;
+          k0 = tile_at(u_begin);
+          k1 = tile_at(u_end);
+          if (k0 < k1) break;
+          if (nt == 0 && u0 >= u_begin) {
+            // No row of the item sees a key (an empty cache, more tokens than keys): written here.
+            const int i0 = p * 2 * geo.tpt, rows = min(s.nq - i0, 2 * geo.tpt) * geo.G;
+#pragma unroll 1
+            for (int r = lane >> 4; r < rows; r += 2) {
+              const int tok = r / geo.G;
+              const long long at = static_cast<long long>(s.tok0 + i0 + tok) * args.Hq + h * geo.G + r - tok * geo.G;
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.o) + at * D + (lane & 15) * 8) = make_uint4(0u, 0u, 0u, 0u);
+              if (args.lse != nullptr && (lane & 15) == 0) args.lse[at] = -INFINITY;
             }
           }
+          u0 += c.item + nt * c.tile;
+          next_item();
         }
+        // A free place in the ring.  Q follows two pieces behind, that of the first two at once.
+#pragma unroll 1
+        while (ok && iq < (ip <= 2 ? ip : ip - 2)) load_q();
+        if (ok && ip >= NP) ok = wait_bar(smem_u32(&sm.piece_empty[ip % NP]), ((ip / NP) - 1) & 1, abort_flag);
+        if (!ok) break;
+        Piece& out = sm.piece[ip % NP];
+        if (stop) {
+          out.stop = 1;
+        } else {
+          const bool single = s.nq - p * 2 * geo.tpt <= geo.tpt;
+          if (!single) slot0 = 0;
+          if (lane == 0) {
+            const int i0 = p * 2 * geo.tpt;
+            out.tok0 = s.tok0 + i0;
+            out.ntok = min(s.nq - i0, 2 * geo.tpt);
+            out.kvh = h;
+            out.b = b;
+            out.j0 = lo / BN + k0;
+            out.j1 = lo / BN + k1;
+            out.key_lo = lo;
+            out.key_hi = hi;
+            out.single = single;
+            out.tile0 = tile0;
+            out.slot0 = slot0;
+            out.part = k0 == 0 && k1 == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (k0 == 0 ? 1 : 0);
+            out.stop = 0;
+            fill_slots(args, geo, out, s.n - s.nq + i0);
+            if (k0 == 0 && k1 < nt) {
+              // The run that holds the last tile's unit, which lies at or past this one's end.
+              const long long past = u0 + c.item + (nt - 1) * c.tile - u_end;
+              const int runs = run > past ? 0 : static_cast<int>(static_cast<unsigned>(past) / static_cast<unsigned>(run));
+              open = ExtendDesc{out.tok0, out.ntok, h, static_cast<int>(blockIdx.x) + 1 + runs};
+            }
+          }
+          tile0 += k1 - k0;
+          if (single) slot0 = (slot0 + k1 - k0) & 1;
+          u0 += c.item + nt * c.tile;
+          next_item();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.piece_full[ip % NP]));
+        ++ip;
       }
-      if (place()) {
-        if (lane == 0) sm.piece[ip % NP].stop = 1;
-        hand_out();
-        while (ok && iq < ip - 1) load_q();
-      }
+#pragma unroll 1
+      while (ok && iq < ip - 1) load_q();
       if (lane == 0) args.desc[blockIdx.x] = open;
       if (nq0 > 0) mbar_wait_drain(smem_u32(&sm.q_full[0]), (nq0 - 1) & 1);
       if (nq1 > 0) mbar_wait_drain(smem_u32(&sm.q_full[1]), (nq1 - 1) & 1);
@@ -657,7 +663,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // blocks of one or two keys, is looked up here).
       auto load_tile = [&](const Piece& p, int j, int id) {
         const int s = n % NS;
-        if (n >= NS) ok = mbar_wait_warp(smem_u32(&empty[s]), ((n / NS) - 1) & 1, abort_flag);
+        if (n >= NS) ok = wait_bar(smem_u32(&empty[s]), ((n / NS) - 1) & 1, abort_flag);
         if (!ok) return;
         const uint32_t bar = smem_u32(&full[s]);
         // Tile n - 4 is done with these words: K's stage was that of tile n - 2, whose S
@@ -680,6 +686,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           unsigned live = __ballot_sync(0xffffffffu, good);
           if (lane == 0) mbar_expect_tx(bar, __popc(live) * rows * 256u);
           __syncwarp();
+#pragma unroll 1
           for (; live; live &= live - 1) {
             const int src = __ffs(live) - 1;
             const int z = __shfl_sync(0xffffffffu, id, src) * args.Hkv + p.kvh;
@@ -694,180 +701,204 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (lane == 0) mbar_arrive(bar);
         ++n;
       };
-      // The first piece from i on that has keys; -1: none is left.
-      auto find = [&](int i) {
-        while (pieces.wait(i)) {
-          if (pieces.at(i).j0 < pieces.at(i).j1) return i;
-          pieces.release(i++, lane);
-        }
-        return -1;
-      };
-      int ip = find(0), j = 0, even = 0, odd = 0;
+      // Piece i's number, -1: there is none.
+      auto find = [&](int i) { return pieces.wait(i) ? i : -1; };
+      // One tile a turn: the next one's entries are asked for, then this one is loaded.
+      int ip = find(0), j = 0, id = 0;
       if (ip >= 0) {
         j = pieces.at(ip).j0;
-        even = lookup(pieces.at(ip), j, lane);
+        id = lookup(pieces.at(ip), j, lane);
       }
-      // One tile: the next one's entries are asked for, then this one is loaded.
-      auto step = [&](int cur, int& next) {
-        int in = ip, jn = j + 1;
+#pragma unroll 1
+      while (ok && ip >= 0) {
+        int in = ip, jn = j + 1, next = 0;
         if (jn == pieces.at(ip).j1) {
           in = find(ip + 1);
           if (in >= 0) jn = pieces.at(in).j0;
         }
         if (in >= 0) next = lookup(pieces.at(in), jn, lane);
-        if (ok) load_tile(pieces.at(ip), j, cur);
+        load_tile(pieces.at(ip), j, id);
         if (in != ip) pieces.release(ip, lane);
         ip = in;
         j = jn;
-      };
-      while (ok && ip >= 0) {
-        step(even, odd);
-        if (ok && ip >= 0) step(odd, even);
+        id = next;
       }
+#pragma unroll 1
       for (int i = max(0, n - NS); i < n; ++i) mbar_wait_drain(smem_u32(&full[i % NS]), (i / NS) & 1);
     } else {
       // ---------------------------------------------------------- MMA issuer
       // The whole warp runs this (warp-uniform waits); MMAs and commits go out from one
-      // elected lane.  Phase bits, bit t for slot t: Q_PH q_full, P_PH p_full and O_PH
-      // o_free to wait for next; O_USED: an item has used O_t.
+      // elected lane.  The work is one stream of steps through the items: a one-tile item
+      // has a step per key tile, a two-tile item two, one per slot.  S of step w + 2 goes out
+      // after PV of step w, in the same slot, so the softmaxes of two steps overlap, of
+      // successive items too.  Phase bits, bit t for slot t: Q_PH q_full, P_PH p_full and
+      // O_PH o_free to wait for next; O_USED: an item has used O_t.
       const uint32_t tiles = tiles_base(), tmem = tmem_base();
       enum : uint32_t { Q_PH = 0, P_PH = 2, O_PH = 4, O_USED = 6 };
       uint32_t ph = 0;
       auto bit = [&](uint32_t i) { return (ph >> i) & 1u; };
       bool ok = true;
-      // g: a key tile's number in the CTA, its place in both rings.
-      auto wait_k = [&](int g) {
-        return mbar_wait_warp(smem_u32(&sm.k_full[g % NS]), static_cast<uint32_t>((g / NS) & 1), abort_flag);
+      auto free_tile = [&](uint64_t* empty, int g) { commit_elect(smem_u32(empty + g % NS)); };
+      // A place in the stream: piece, key tile, slot, the tile's number in the CTA.
+      struct Step {
+        int i, j, t, g;
       };
-      auto free_k = [&](int g) { commit_elect(smem_u32(&sm.k_empty[g % NS])); };
-      auto free_v = [&](int g) { commit_elect(smem_u32(&sm.v_empty[g % NS])); };
-      // S_t of tile g from Q slot qs; `first`, `last`: the item's uses of that Q slot.
-      auto issue_s = [&](int t, int qs, int g, bool first, bool last) {
-        if (first) {
-          if (!mbar_wait_warp(smem_u32(&sm.q_full[qs]), bit(Q_PH + qs), abort_flag)) return false;
-          ph ^= 1u << (Q_PH + qs);
-        }
-        issue_qk<T>(tmem + 128 * t, tiles + qs * TILE_BYTES, tiles + kKOff + g % NS * TILE_BYTES);
-        commit_elect(smem_u32(&sm.s_full[t]));
-        if (last) commit_elect(smem_u32(&sm.q_empty[qs]));
-        return true;
+      auto open_piece = [&](Step& at) {
+        const Piece& p = pieces.at(at.i);
+        at.j = p.j0;
+        at.t = p.slot0;
+        at.g = p.tile0;
       };
-      // PV_t of tile g, once P is there.  The slot's first of an item overwrites O_t (which
-      // the epilogue must have read out), its last publishes it.
-      auto issue_o = [&](int t, int g, int2 steps, bool first, bool last) {
-        if (first && bit(O_USED + t)) {
-          if (!mbar_wait_warp(smem_u32(&sm.o_free[t]), bit(O_PH + t), abort_flag)) return false;
-          ph ^= 1u << (O_PH + t);
-        }
-        if (!mbar_wait_warp(smem_u32(&sm.p_full[t]), bit(P_PH + t), abort_flag)) return false;
+      // Is this the step's key tile's last step?  (Two-tile items: slot 1's.)
+      auto last_of_tile = [&](const Piece& p, const Step& at) { return p.single || at.t == 1; };
+      // To the next step of the piece; false past its last.
+      auto advance = [&](const Piece& p, Step& at) {
+        const bool next_tile = last_of_tile(p, at);
+        at.t ^= 1;
+        at.j += next_tile;
+        at.g += next_tile;
+        return at.j < p.j1;
+      };
+      auto k_landed = [&](int g) {
+        return wait_bar(smem_u32(&sm.k_full[g % NS]), static_cast<uint32_t>((g / NS) & 1), abort_flag);
+      };
+      auto v_landed = [&](int g) {
+        return wait_bar(smem_u32(&sm.v_full[g % NS]), static_cast<uint32_t>((g / NS) & 1), abort_flag);
+      };
+      auto p_there = [&](int t) {
+        if (!wait_bar(smem_u32(&sm.p_full[t]), bit(P_PH + t), abort_flag)) return false;
         ph ^= 1u << (P_PH + t);
         tc_fence_after();
-        const uint32_t v = tiles + kVOff + g % NS * TILE_BYTES;
-        if (steps.x == 0 && steps.y == BN / 16) {
-          issue_pv<T>(tmem + 256 + 128 * t, tmem + 128 * t, v, first ? 0u : 1u);
-        } else {
-#pragma unroll 1
-          for (int i = steps.x; i < steps.y; ++i)
-            issue_pv_step<T>(tmem + 256 + 128 * t, tmem + 128 * t + 8 * i, v + i * 16 * 128, first && i == steps.x ? 0u : 1u);
-        }
-        if (last) {
-          commit_elect(smem_u32(&sm.o_full[t]));
-          ph |= 1u << (O_USED + t);
-        }
         return true;
       };
-      // V of tile j of piece p (number g) has landed.  Rows without a key of the item are kept
-      // out of the product: whole steps of 16 keys are not issued (`steps`: first and end),
-      // the others' rows, and those of blocks outside the pool, are cleared.
-      auto ready_v = [&](const Piece& p, int j, int g, bool edge, int2& steps) {
-        if (!mbar_wait_warp(smem_u32(&sm.v_full[g % NS]), static_cast<uint32_t>((g / NS) & 1), abort_flag)) return false;
-        steps = make_int2(0, BN / 16);
+      auto any_bad = [&](int g) {
         const uint4 bad = *reinterpret_cast<const uint4*>(sm.bad[g & 3]);
-        const bool any_bad = (bad.x | bad.y | bad.z | bad.w) != 0u;
-        if (!edge && !any_bad) return true;
-        const int lo = max(0, p.key_lo - j * BN), hi = min(BN, p.key_hi - j * BN);
-        steps = make_int2(lo >> 4, (hi + 15) >> 4);
-        if ((lo & 15) != 0 || (hi & 15) != 0 || any_bad) {
-          const uint32_t v = tiles + kVOff + g % NS * TILE_BYTES;
-          zero_v_rows(v, lo & ~15, lo, lane);
-          zero_v_rows(v, hi, (hi + 15) & ~15, lane);
-          if (any_bad) zero_bad_rows(v, sm.bad[g & 3], lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        return true;
+        return (bad.x | bad.y | bad.z | bad.w) != 0u;
       };
-      // One-tile items: their key tiles form one stream through the items.  S runs up to two
-      // tiles ahead of PV, S of tile g + 2 following PV of tile g in its slot, so that the
-      // softmaxes of two tiles (of the same or of successive items) overlap.
-      int is = 0, sj = 0, gs = 0, np = 0;  // S's piece, its next tile, that one's number; items begun
-      bool s_open = false;
-      auto advance_s = [&]() {
-        while (!s_open) {
-          if (!pieces.wait(is)) return false;
-          const Piece& p = pieces.at(is);
-          if (p.j0 < p.j1) {
-            if (!p.single) return false;  // two-tile items issue their own
-            s_open = true;
-            sj = p.j0;
-          } else {
-            ++is;
-          }
-        }
-        const Piece& p = pieces.at(is);
-        const bool last = sj + 1 == p.j1;
-        ok = wait_k(gs) && issue_s(gs & 1, np & 1, gs, sj == p.j0, last);
-        if (!ok) return false;
-        free_k(gs);
-        ++gs;
-        ++sj;
-        if (last) {
-          s_open = false;
-          ++is;
-          ++np;
-        }
-        return true;
-      };
-      int g = 0;  // the number of the next tile to take its PV
-      for (int ip = 0; ok && pieces.wait(ip); pieces.release(ip++, lane)) {
-        const Piece& p = pieces.at(ip);
-        if (p.j0 == p.j1) continue;
-        if (p.single) {
-          for (int j = p.j0; ok && j < p.j1; ++j, ++g) {
-            while (gs < g + 2 && advance_s()) {
+      Step sc{0, 0, 0, 0}, oc{0, -1, 0, 0};  // the next S, the next PV (j = -1: its piece is to be opened)
+      int ahead = 0;                         // steps that S is ahead of PV
+      bool s_more = pieces.wait(0);
+      if (s_more) open_piece(sc);
+      bool hold = false;  // the next S's slot is the last one's: it waits for that one's PV
+      int2 steps = make_int2(0, 0);
+#pragma unroll 1
+      while (ok && (s_more || ahead > 0)) {
+        const bool do_o = ahead == 2 || !s_more || (hold && ahead == 1);
+        const bool do_s = s_more && !(hold && ahead - do_o > 0);
+        if (do_o && oc.j < 0) open_piece(oc);
+        if (do_o && do_s && sc.i == oc.i && oc.t == 0) {
+          // Inside a two-tile item, away from its edges: the same steps without their questions.
+          const Piece& p = pieces.at(oc.i);
+          const int end = p.single ? 0 : min(p.end[0], p.end[1]) - 2;
+          if (oc.j < end && oc.j > max(p.first[0], p.first[1])) {
+            int g = oc.g;
+            const int g_end = g + end - oc.j;
+#pragma unroll 1
+            for (; g < g_end; ++g) {
+              ok = v_landed(g) && k_landed(g + 1);
+              if (!ok || any_bad(g)) break;
+              const uint32_t k = tiles + kKOff + (g + 1) % NS * TILE_BYTES, v = tiles + kVOff + g % NS * TILE_BYTES;
+#pragma unroll 1
+              for (int t = 0; t < 2; ++t) {
+                if (!(ok = p_there(t))) break;
+                issue_pv<T>(tmem + 256 + 128 * t, tmem + 128 * t, v, 1u);
+                if (t) free_tile(sm.v_empty, g);
+                issue_qk<T>(tmem + 128 * t, tiles + t * TILE_BYTES, k);
+                commit_elect(smem_u32(&sm.s_full[t]));
+              }
+              if (!ok) break;
+              free_tile(sm.k_empty, g + 1);
             }
-            int2 steps;
-            ok = ok && ready_v(p, j, g, j == p.j0 || j + 1 == p.j1, steps) &&
-                 issue_o(g & 1, g, steps, j < p.j0 + 2, j + 2 >= p.j1);
-            if (ok) free_v(g);
-          }
-        } else {
-          // Two row tiles, a slot each: PV_0, next S_0, PV_1, next S_1.
-          const int a0 = p.first[0], b0 = p.end[0], a1 = p.first[1], b1 = p.end[1], j1 = p.j1;
-          auto in0 = [&](int k) { return k >= a0 && k < b0; };
-          auto in1 = [&](int k) { return k >= a1 && k < b1; };
-          int j = p.j0;
-          ok = wait_k(g);
-          if (ok && in0(j)) ok = issue_s(0, 0, g, true, j == b0 - 1);
-          if (ok && in1(j)) ok = issue_s(1, 1, g, true, j == b1 - 1);
-          if (ok) free_k(g);
-          for (; ok && j < j1; ++j, ++g) {
-            const bool next = j + 1 < j1;
-            int2 steps;
-            ok = ready_v(p, j, g, j == p.j0 || !next, steps) && (!next || wait_k(g + 1));
-            if (ok && in0(j)) ok = issue_o(0, g, steps, j == a0, j == b0 - 1);
-            if (ok && next && in0(j + 1)) ok = issue_s(0, 0, g + 1, j + 1 == a0, j + 1 == b0 - 1);
-            if (ok && in1(j)) ok = issue_o(1, g, steps, j == a1, j == b1 - 1);
             if (!ok) break;
-            free_v(g);
-            if (next) {
-              if (in1(j + 1)) ok = issue_s(1, 1, g + 1, j + 1 == a1, j + 1 == b1 - 1);
-              if (ok) free_k(g + 1);
+            const int done = g - oc.g;
+            oc.j += done;
+            oc.g += done;
+            sc.j += done;
+            sc.g += done;
+          }
+        }
+        if (do_s) {
+          // K and, for its first use, Q have landed: waited for ahead of the PV, so that the
+          // two follow one another into the tensor pipe.
+          const Piece& p = pieces.at(sc.i);
+          if (sc.j == (p.single ? p.j0 : p.first[sc.t]) && sc.j < p.end[sc.t]) {
+            const int qs = p.single ? sc.i & 1 : sc.t;
+            ok = wait_bar(smem_u32(&sm.q_full[qs]), bit(Q_PH + qs), abort_flag);
+            ph ^= 1u << (Q_PH + qs);
+          }
+          ok = ok && k_landed(sc.g);
+          if (!ok) break;
+        }
+        if (do_o) {
+          const Piece& p = pieces.at(oc.i);
+          const int t = oc.t;
+          const uint32_t v = tiles + kVOff + oc.g % NS * TILE_BYTES;
+          if (p.single || t == 0) {
+            // V has landed.  Rows without a key of the item are kept out of the product: whole
+            // steps of 16 keys are not issued (`steps`: first and end), the others' rows, and
+            // those of blocks outside the pool, are cleared.
+            ok = v_landed(oc.g);
+            if (!ok) break;
+            const int lo = max(0, p.key_lo - oc.j * BN), hi = min(BN, p.key_hi - oc.j * BN);
+            steps = make_int2(lo >> 4, (hi + 15) >> 4);
+            const bool bad = any_bad(oc.g);
+            if ((lo & 15) != 0 || (hi & 15) != 0 || bad) {
+              zero_v_rows(v, lo & ~15, lo, lane);
+              zero_v_rows(v, hi, (hi + 15) & ~15, lane);
+              if (bad) zero_bad_rows(v, sm.bad[oc.g & 3], lane);
+              fence_proxy_async_smem();
+              __syncwarp();
             }
           }
-          is = ip + 1;
-          gs = g;
-          ++np;
+          if (oc.j >= p.first[t] && oc.j < p.end[t]) {
+            // The slot's first PV of the item overwrites O_t (which the epilogue must have read
+            // out), its last publishes it.
+            const bool first = oc.j == p.first[t], last = oc.j + (p.single ? 2 : 1) >= p.end[t];
+            if (first && bit(O_USED + t)) {
+              ok = wait_bar(smem_u32(&sm.o_free[t]), bit(O_PH + t), abort_flag);
+              ph ^= 1u << (O_PH + t);
+            }
+            ok = ok && p_there(t);
+            if (!ok) break;
+            if (steps.x == 0 && steps.y == BN / 16) {
+              issue_pv<T>(tmem + 256 + 128 * t, tmem + 128 * t, v, first ? 0u : 1u);
+            } else {
+#pragma unroll 1
+              for (int i = steps.x; i < steps.y; ++i)
+                issue_pv_step<T>(tmem + 256 + 128 * t, tmem + 128 * t + 8 * i, v + i * 16 * 128, first && i == steps.x ? 0u : 1u);
+            }
+            if (last) {
+              commit_elect(smem_u32(&sm.o_full[t]));
+              ph |= 1u << (O_USED + t);
+            }
+          }
+          if (last_of_tile(p, oc)) free_tile(sm.v_empty, oc.g);
+          --ahead;
+          if (!advance(p, oc)) {
+            pieces.release(oc.i++, lane);
+            oc.j = -1;
+          }
+        }
+        if (do_s) {
+          const Piece& p = pieces.at(sc.i);
+          if (sc.j >= p.first[sc.t] && sc.j < p.end[sc.t]) {
+            const int qs = p.single ? sc.i & 1 : sc.t;
+            issue_qk<T>(tmem + 128 * sc.t, tiles + qs * TILE_BYTES, tiles + kKOff + sc.g % NS * TILE_BYTES);
+            commit_elect(smem_u32(&sm.s_full[sc.t]));
+            if (sc.j + 1 == (p.single ? p.j1 : p.end[sc.t])) commit_elect(smem_u32(&sm.q_empty[qs]));
+          }
+          if (last_of_tile(p, sc)) free_tile(sm.k_empty, sc.g);
+          ++ahead;
+          hold = false;
+          if (!advance(p, sc)) {
+            const int t = sc.t ^ 1;  // the slot of the step just issued
+            ++sc.i;
+            s_more = pieces.wait(sc.i);
+            if (s_more) {
+              open_piece(sc);
+              hold = sc.t == t;
+            }
+          }
         }
       }
       // All MMAs issued by this warp must complete before TMEM is freed.
@@ -889,15 +920,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t stage = tiles_base() + kStageOff + wq * kStageBytes;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     uint32_t ph = 0;  // phase of o_full (and st_full) to wait for next, bit t for slot t
-    int base = 0;     // key tiles of the pieces before this one
     bool ok = true;
+#pragma unroll 1
     for (int ip = 0; ok && pieces.wait(ip); pieces.release(ip++, lane)) {
       const Piece& p = pieces.at(ip);
-      const int slot = p.slot;
+      const int slot = p.part;
+#pragma unroll 1
       for (int rt = 0; rt < (p.single ? 1 : 2) && ok; ++rt) {
         // t: the slot; of a one-tile item's two, the one whose last tile comes last.
         const int nt = p.j1 - p.j0;
-        const int t = p.single ? (base + nt - 1) & 1 : rt;
+        const int t = p.single ? (p.slot0 + nt - 1) & 1 : rt;
         const bool both = p.single && nt > 1;
         const int mine = p.rows[rt] - wq * 32;  // rows of this warp's 32 that hold a token, if positive
         // This row's place in the output or, for a piece, in the workspace.
@@ -908,8 +940,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           at = static_cast<long long>(slot) * args.slot_rows + rt * BM + row;
         }
         float* lse = slot < 0 ? args.lse : args.ws_lse;
-        if (nt == 0 || !p.any(t)) {
-          // No key tile: a whole item's rows see nothing; a piece adds nothing.
+        if (!p.any(t)) {
+          // A row tile without keys beside one that has some: its rows see nothing; of a piece,
+          // they may see something in another one.
           if (lane < mine) {
             if (lse != nullptr) lse[at] = -INFINITY;
             if (slot < 0) {
@@ -925,8 +958,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (both) {
           // The other slot is done one tile earlier.  With a few rows its O is put aside in the
           // stage, so that the next item's first tile finds the slot free.
-          ok = mbar_wait_warp(smem_u32(&sm.o_full[t ^ 1]), ph >> (t ^ 1) & 1u, abort_flag) &&
-               mbar_wait_warp(smem_u32(&sm.st_full[t ^ 1]), ph >> (t ^ 1) & 1u, abort_flag);
+          ok = wait_bar(smem_u32(&sm.o_full[t ^ 1]), ph >> (t ^ 1) & 1u, abort_flag) &&
+               wait_bar(smem_u32(&sm.st_full[t ^ 1]), ph >> (t ^ 1) & 1u, abort_flag);
           if (!ok) break;
           ph ^= 1u << (t ^ 1);
           tc_fence_after();
@@ -954,8 +987,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_arrive(smem_u32(&sm.o_free[t ^ 1]));
           }
         }
-        ok = mbar_wait_warp(smem_u32(&sm.o_full[t]), ph >> t & 1u, abort_flag) &&
-             mbar_wait_warp(smem_u32(&sm.st_full[t]), ph >> t & 1u, abort_flag);
+        ok = wait_bar(smem_u32(&sm.o_full[t]), ph >> t & 1u, abort_flag) &&
+             wait_bar(smem_u32(&sm.st_full[t]), ph >> t & 1u, abort_flag);
         if (!ok) break;
         ph ^= 1u << t;
         tc_fence_after();
@@ -1060,7 +1093,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mbar_arrive(smem_u32(&sm.o_free[t]));
         if (both && !staged) mbar_arrive(smem_u32(&sm.o_free[t ^ 1]));
       }
-      base += p.j1 - p.j0;
     }
   } else {
     // ------------------------------------------------------------ softmax warps
@@ -1078,8 +1110,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // Phase bits: S_PH s_full to wait for next, ST_PH st_empty, ST_ANY an item was published.
     enum : uint32_t { S_PH = 1, ST_PH = 2, ST_ANY = 4 };
     uint32_t ph = ST_PH;
-    int base = 0;  // key tiles of the pieces before this one
     bool ok = true;
+#pragma unroll 1
     for (int ip = 0; ok && pieces.wait(ip); ++ip) {
       // Keys that this row sees, [row_lo, row_hi), and that every row of the tile sees,
       // [all_lo, all_hi): key tiles inside the latter need no mask.
@@ -1091,8 +1123,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         j = p.first[t];
         end = p.end[t];
         step = p.single ? 2 : 1;
-        bad_at = base - p.j0;
-        base += p.j1 - p.j0;
+        bad_at = p.tile0 - p.j0;
         busy = wq * 32 < p.rows[t];
         row_lo = p.key_lo;
         row_hi = p.key_hi;
@@ -1106,8 +1137,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (j >= end) continue;
       float m = -INFINITY, l = 0.f;
       bool nan_row = false, begun = false;
+#pragma unroll 1
       for (; j < end; j += step) {
-        ok = mbar_wait_warp(smem_u32(&sm.s_full[t]), ph & S_PH, abort_flag);
+        ok = wait_bar(smem_u32(&sm.s_full[t]), ph & S_PH, abort_flag);
         if (!ok) break;
         ph ^= S_PH;
         if (!busy) {
@@ -1218,7 +1250,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       if (!ok) break;
-      if (ph & ST_ANY) ok = mbar_wait_warp(smem_u32(&sm.st_empty[t]), (ph & ST_PH) != 0u, abort_flag);
+      if (ph & ST_ANY) ok = wait_bar(smem_u32(&sm.st_empty[t]), (ph & ST_PH) != 0u, abort_flag);
       if (!ok) break;
       ph = (ph ^ ST_PH) | ST_ANY;
       sm.stat_m[t][row] = m;
@@ -1229,6 +1261,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && sm.abort_flag) atomicOr(&g_status, kStatusTimeout);
   if (warp == MMA_WARP) {
     tc_fence_after();
     tmem_dealloc(sm.tmem_base, 512);
