@@ -1155,22 +1155,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const int c_lo = max(0, row_lo - kb), c_hi = max(min(BN, row_hi - kb), c_lo);
 #pragma unroll 1
           for (int c = 0; c < BN / 32; ++c) {
-            const uint32_t bw = sm.bad[(bad_at + j) & 3][c];
-            if (bw == 0u && __all_sync(0xffffffffu, c_lo <= 32 * c && c_hi >= 32 * c + 32)) continue;
+            // Bit e: column 32 c + e is visible.
+            const int lo = min(max(c_lo - 32 * c, 0), 32), hi = min(max(c_hi - 32 * c, 0), 32);
+            const uint32_t seen = (hi == 32 ? 0xffffffffu : (1u << hi) - 1u) & (lo == 32 ? 0u : 0xffffffffu << lo) &
+                                  ~sm.bad[(bad_at + j) & 3][c];
+            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
             uint32_t r[32];
-            if (__all_sync(0xffffffffu, c_hi <= 32 * c || c_lo >= 32 * c + 32)) {
+            FA_TMEM_LD32(tS + 32 * c, r);
+            tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(-INFINITY);
-            } else {
-              FA_TMEM_LD32(tS + 32 * c, r);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = keep_or_ninf(r[e], 32 * c + e, c_lo, c_hi);
-              if (bw != 0u) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) r[e] = (bw >> e) & 1u ? __float_as_uint(-INFINITY) : r[e];
-              }
-            }
+            for (int e = 0; e < 32; ++e) r[e] = seen >> e & 1u ? r[e] : __float_as_uint(-INFINITY);
             FA_TMEM_ST32(tS + 32 * c, r);
           }
           tmem_st_wait();
