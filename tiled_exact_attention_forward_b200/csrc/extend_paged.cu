@@ -66,8 +66,8 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
 struct Cost {
   int item, tile;
 };
-constexpr int kItemUnits1 = 4, kTileUnits1 = 2, kItemUnits2 = 7, kTileUnits2 = 3;  // items of one, two row tiles
-constexpr int kMinUnits = 6;
+constexpr int kItemUnits1 = 3, kTileUnits1 = 2, kItemUnits2 = 7, kTileUnits2 = 3;  // items of one, two row tiles
+constexpr int kMinUnits = 2;
 // The planner keeps the units of so many sequences; it works those of more out twice.
 constexpr int kPlanSeqs = 1024;
 // Epilogue: up to so many rows of a warp are written by their own lanes; more go through
