@@ -52,8 +52,8 @@ constexpr int V_WARP = 15;                  // V tiles
 constexpr int NP = 8;                       // pieces in flight between the planner and the other warps
 constexpr int kPieceReaders = 15;           // warps that read a piece: MMA, K, V, 8 softmax, 4 epilogue
 constexpr int kSoftmaxRegs = 184;
-constexpr int kEpilogueRegs = 80;
-constexpr int kOtherRegs = 64;
+constexpr int kEpilogueRegs = 72;
+constexpr int kOtherRegs = 72;
 constexpr int kLaunchRegs = 128;            // 65536 / NUM_THREADS: what the split draws on
 static_assert(2 * WG_THREADS * kSoftmaxRegs + WG_THREADS * kEpilogueRegs + WG_THREADS * kOtherRegs <=
                   NUM_THREADS * kLaunchRegs,
@@ -67,12 +67,15 @@ struct Cost {
   int item, tile;
 };
 constexpr int kItemUnits1 = 3, kTileUnits1 = 2, kItemUnits2 = 7, kTileUnits2 = 3;  // items of one, two row tiles
-constexpr int kMinUnits = 2;
+constexpr int kMinUnits = 3;
+// Every run inside an item then holds the first unit of some key tile, so that each of the
+// CTAs between an item's first and last has a piece of it (combine_kernel reads them all).
+static_assert(kMinUnits >= kTileUnits1 && kMinUnits >= kTileUnits2, "runs without a piece");
 // The planner keeps the units of so many sequences; it works those of more out twice.
 constexpr int kPlanSeqs = 1024;
-// Epilogue: up to so many rows of a warp are written by their own lanes; more go through
-// shared memory, so that a store instruction does not touch 32 lines.
-constexpr int kDirectRows = 8;
+// Epilogue: an item of so many rows at most (one warp's) has its first finished slot put
+// aside in shared memory.
+constexpr int kAsideRows = 32;
 
 // A wait gives up after so many cycles.
 constexpr unsigned kWaitCycles = 2000000000u;
@@ -98,13 +101,12 @@ struct Piece {
   __device__ __forceinline__ bool any(int t) const { return first[t] < end[t]; }
 };
 
-// Dynamic shared memory, 1024-byte aligned: Q tiles, K ring, V ring, then the epilogue's
-// staging, 32 rows of 128 bytes per warp.
+// Dynamic shared memory, 1024-byte aligned: Q tiles, K ring, V ring, then kAsideRows rows
+// of float32 that the epilogue puts aside.
 constexpr int kKOff = 2 * TILE_BYTES;
 constexpr int kVOff = kKOff + NS * TILE_BYTES;
-constexpr int kStageOff = kVOff + NS * TILE_BYTES;
-constexpr int kStageBytes = 32 * 128;
-constexpr size_t kSmemBytes = kStageOff + 4 * kStageBytes + 1024;
+constexpr int kAsideOff = kVOff + NS * TILE_BYTES;
+constexpr size_t kSmemBytes = kAsideOff + kAsideRows * D * 4 + 1024;
 
 // Heads per key head and tokens per row tile, 128 / G.
 struct Geo {
@@ -917,7 +919,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const Geo geo = geometry();
     const int row_tok = row / geo.G;
     const uint32_t tmem = tmem_base();
-    const uint32_t stage = tiles_base() + kStageOff + wq * kStageBytes;
+    // This lane's row put aside; 16-byte chunk i of it sits at chunk i ^ lane.
+    const uint32_t aside = tiles_base() + kAsideOff + lane * (D * 4);
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     uint32_t ph = 0;  // phase of o_full (and st_full) to wait for next, bit t for slot t
     bool ok = true;
@@ -954,10 +957,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           continue;
         }
         float m1 = -INFINITY, l1 = 0.f;
-        bool staged = false;
+        bool put_aside = false;
         if (both) {
-          // The other slot is done one tile earlier.  With a few rows its O is put aside in the
-          // stage, so that the next item's first tile finds the slot free.
+          // The other slot is done one tile earlier.  With few rows its O is put aside, so that
+          // the next item's first tile finds the slot free.
           ok = wait_bar(smem_u32(&sm.o_full[t ^ 1]), ph >> (t ^ 1) & 1u, abort_flag) &&
                wait_bar(smem_u32(&sm.st_full[t ^ 1]), ph >> (t ^ 1) & 1u, abort_flag);
           if (!ok) break;
@@ -966,8 +969,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           m1 = sm.stat_m[t ^ 1][row];
           l1 = sm.stat_l[t ^ 1][row];
           mbar_arrive(smem_u32(&sm.st_empty[t ^ 1]));
-          staged = p.rows[0] <= kDirectRows;
-          if (staged) {
+          put_aside = p.rows[0] <= kAsideRows;
+          if (put_aside) {
             if (mine > 0) {
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
@@ -977,7 +980,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (lane < mine) {
 #pragma unroll
                   for (int v = 0; v < 8; ++v)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * (D * 4) + c * 4 + v * 16),
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(aside + ((c / 4 + v) ^ lane) * 16),
                                  "r"(r[4 * v]), "r"(r[4 * v + 1]), "r"(r[4 * v + 2]), "r"(r[4 * v + 3])
                                  : "memory");
                 }
@@ -1013,21 +1016,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool part = slot >= 0;
         char* out = part ? reinterpret_cast<char*>(args.ws_o) : static_cast<char*>(args.o);
         at *= part ? D * 4 : D * 2;  // bytes from here on
-        if (mine > 0 && mine <= kDirectRows) {
-          // A few rows: each lane writes its own.
+        if (mine > 0) {
+          // Each lane writes its own row, 32 or 64 bytes a step.  (Rows put_aside in shared memory and
+          // written in runs of 128 bytes were no faster: 107 us for 108 on the ragged batch.)
           char* dst = out + at;
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             float o[16];
-            load_o16(tO + c, tO1 + c, both && !staged, none, f0, f1, o);
+            load_o16(tO + c, tO1 + c, both && !put_aside, none, f0, f1, o);
             if (lane < mine) {
-              if (staged && !none) {
+              if (put_aside && !none) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                   float4 x;
                   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                                : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                               : "r"(stage + lane * (D * 4) + c * 4 + v * 16));
+                               : "r"(aside + ((c / 4 + v) ^ lane) * 16));
                   o[4 * v] = fmaf(x.x, f1, o[4 * v]);
                   o[4 * v + 1] = fmaf(x.y, f1, o[4 * v + 1]);
                   o[4 * v + 2] = fmaf(x.z, f1, o[4 * v + 2]);
@@ -1047,51 +1051,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               }
             }
           }
-        } else if (mine > 0) {
-          // Staged: 64 16-bit or 32 float32 columns fill 128 bytes a row, which go out in runs,
-          // eight lanes a row.  16-byte chunk i of a row sits at chunk i ^ (row % 8).
-          const uint32_t dst = stage + lane * 128, sw = (lane & 7) << 4;
-          const int cols = part ? 32 : 64;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            float o[16];
-            load_o16(tO + c, tO1 + c, both, none, f0, f1, o);
-            const int in = c & (cols - 1);
-            if (in == 0) __syncwarp();  // the stage's last rows have been read
-            if (part) {
-#pragma unroll
-              for (int v = 0; v < 4; ++v)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((in * 4 + v * 16) ^ sw)),
-                             "f"(o[4 * v]), "f"(o[4 * v + 1]), "f"(o[4 * v + 2]), "f"(o[4 * v + 3])
-                             : "memory");
-            } else {
-#pragma unroll
-              for (int v = 0; v < 2; ++v)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((in * 2 + v * 16) ^ sw)),
-                             "r"(pack2<T>(o[8 * v], o[8 * v + 1])), "r"(pack2<T>(o[8 * v + 2], o[8 * v + 3])),
-                             "r"(pack2<T>(o[8 * v + 4], o[8 * v + 5])), "r"(pack2<T>(o[8 * v + 6], o[8 * v + 7]))
-                             : "memory");
-            }
-            if (in == cols - 16) {
-              __syncwarp();
-              const int ch = (lane & 7) << 4;
-#pragma unroll 2
-              for (int r = lane >> 3; r < 32; r += 4) {
-                const long long row_at = __shfl_sync(0xffffffffu, at, r);
-                uint4 v;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                             : "r"(stage + r * 128 + (ch ^ ((r & 7) << 4))));
-                if (r < mine) *reinterpret_cast<uint4*>(out + row_at + ch) = v;
-              }
-              at += 128;
-            }
-          }
-          __syncwarp();  // the stage may be written otherwise next
         }
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.o_free[t]));
-        if (both && !staged) mbar_arrive(smem_u32(&sm.o_free[t ^ 1]));
+        if (both && !put_aside) mbar_arrive(smem_u32(&sm.o_free[t ^ 1]));
       }
     }
   } else {
