@@ -17,8 +17,8 @@
 //                 S -> softmax -> PV chain of one key tile overlaps the next one's;
 //                 the epilogue joins the two states.
 //
-// Work split.  One persistent CTA per SM.  Items and their key tiles cost units (Cost
-// below); all items laid end to end are cut into equal runs of units, one per CTA,
+// Work split.  One persistent CTA per SM.  Items and their key tiles cost units
+// (kTileUnits below); all items laid end to end are cut into equal runs of units, one per CTA,
 // whatever the lengths: a long sequence with few rows is spread over many CTAs,
 // many short ones share a CTA.  An item cut by a run's edge leaves normalised float32
 // partials and their logsumexp in the workspace, and combine_kernel joins them (in
@@ -59,18 +59,16 @@ static_assert(2 * WG_THREADS * kSoftmaxRegs + WG_THREADS * kEpilogueRegs + WG_TH
                   NUM_THREADS * kLaunchRegs,
               "register split exceeds the launch budget");
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
-// Costs in units of about 0.7 us, from a fit of the CTAs' times on mixed batches: a key
-// tile of a one-tile item 1.3-1.5 us (its bytes at the memory's rate), of a two-tile item
-// 1.8-2.9 us, an item itself 2-3.6 us and 5 us.  A CTA takes at least kMinUnits, so that few
-// keys are not scattered over so many CTAs that joining them costs more than it saves.
-struct Cost {
-  int item, tile;
-};
-constexpr int kItemUnits1 = 3, kTileUnits1 = 2, kItemUnits2 = 7, kTileUnits2 = 3;  // items of one, two row tiles
-constexpr int kMinUnits = 3;
-// Every run inside an item then holds the first unit of some key tile, so that each of the
-// CTAs between an item's first and last has a piece of it (combine_kernel reads them all).
-static_assert(kMinUnits >= kTileUnits1 && kMinUnits >= kTileUnits2, "runs without a piece");
+// Costs in units of about 0.7 us.  A key tile of a one-tile item took 1.3-1.5 us (its bytes
+// at the memory's rate), of a two-tile item 1.8-2.9 us; weights of 2 and 3 served mixed
+// batches no better than 2 and 2 (ragged batch without a window 145 and 136 us), and equal
+// ones let a run be a single tile.  An item itself: 3 and 5 (4 and 7: 2 % slower on single
+// tokens, 2 and 4: 2 % slower on ragged batches).
+constexpr int kTileUnits = 2, kItemUnits1 = 3, kItemUnits2 = 5;  // items of one, two row tiles
+// A CTA takes at least so many.  Every run inside an item then holds the first unit of some
+// key tile, so that each of the CTAs between an item's first and last has a piece of it
+// (combine_kernel reads them all).
+constexpr int kMinUnits = kTileUnits;
 // The planner keeps the units of so many sequences; it works those of more out twice.
 constexpr int kPlanSeqs = 1024;
 // Epilogue: an item of so many rows at most (one warp's) has its first finished slot put
@@ -174,14 +172,13 @@ __device__ __forceinline__ int item_tiles(const ExtendArgs& a, const Geo& g, con
   key_range(a, s.n - s.nq + i0, s.n - s.nq + i1 - 1, s.n, lo, hi);
   return hi > lo ? (hi + BN - 1) / BN - lo / BN : 0;
 }
-// Costs of item p of the sequence, and its units.
-__device__ __forceinline__ Cost cost_of(const Geo& g, const Seq& s, int p) {
-  return s.nq - p * 2 * g.tpt > g.tpt ? Cost{kItemUnits2, kTileUnits2} : Cost{kItemUnits1, kTileUnits1};
+// Units of item p of the sequence ahead of its first key tile, and in all.
+__device__ __forceinline__ int head_cost(const Geo& g, const Seq& s, int p) {
+  return s.nq - p * 2 * g.tpt > g.tpt ? kItemUnits2 : kItemUnits1;
 }
 __device__ __forceinline__ int item_units(const ExtendArgs& a, const Geo& g, const Seq& s, int p) {
   int lo, hi;
-  const Cost c = cost_of(g, s, p);
-  return c.item + item_tiles(a, g, s, p, lo, hi) * c.tile;
+  return head_cost(g, s, p) + item_tiles(a, g, s, p, lo, hi) * kTileUnits;
 }
 __device__ __forceinline__ int items_of(const Geo& g, int nq) { return (nq + 2 * g.tpt - 1) / (2 * g.tpt); }
 
@@ -558,20 +555,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll 1
       for (bool stop = false; ok && !stop;) {
         int nt = 0, lo = 0, hi = 0, k0 = 0, k1 = 0;
-        Cost c{0, 0};
+        int head = 0;
         // To the next item with a key tile in the run.
 #pragma unroll 1
         while (true) {
           stop = u0 >= u_end;
           if (stop) break;
           nt = item_tiles(args, geo, s, p, lo, hi);
-          c = cost_of(geo, s, p);
-          // Tile k of the item begins at unit t0 + k c.tile, and the run that holds this unit
+          head = head_cost(geo, s, p);
+          // Tile k of the item begins at unit t0 + k kTileUnits, and the run that holds this unit
           // takes it; unit u0 only says who writes an item without keys.
-          const long long t0 = u0 + c.item;
+          const long long t0 = u0 + head;
           auto tile_at = [&](long long u) {
-            const int x = static_cast<int>(min(max(u - t0, 0LL), static_cast<long long>(nt * c.tile)));
-            return c.tile == kTileUnits1 ? (x + kTileUnits1 - 1) / kTileUnits1 : (x + kTileUnits2 - 1) / kTileUnits2;
+            const int x = static_cast<int>(min(max(u - t0, 0LL), static_cast<long long>(nt) * kTileUnits));
+            return (x + kTileUnits - 1) / kTileUnits;
           };
           k0 = tile_at(u_begin);
           k1 = tile_at(u_end);
@@ -587,7 +584,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if (args.lse != nullptr && (lane & 15) == 0) args.lse[at] = -INFINITY;
             }
           }
-          u0 += c.item + nt * c.tile;
+          u0 += head + static_cast<long long>(nt) * kTileUnits;
           next_item();
         }
         // A free place in the ring.  Q follows two pieces behind, that of the first two at once.
@@ -619,14 +616,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             fill_slots(args, geo, out, s.n - s.nq + i0);
             if (k0 == 0 && k1 < nt) {
               // The run that holds the last tile's unit, which lies at or past this one's end.
-              const long long past = u0 + c.item + (nt - 1) * c.tile - u_end;
+              const long long past = u0 + head + (nt - 1LL) * kTileUnits - u_end;
               const int runs = run > past ? 0 : static_cast<int>(static_cast<unsigned>(past) / static_cast<unsigned>(run));
               open = ExtendDesc{out.tok0, out.ntok, h, static_cast<int>(blockIdx.x) + 1 + runs};
             }
           }
           tile0 += k1 - k0;
           if (single) slot0 = (slot0 + k1 - k0) & 1;
-          u0 += c.item + nt * c.tile;
+          u0 += head + static_cast<long long>(nt) * kTileUnits;
           next_item();
         }
         __syncwarp();
