@@ -69,6 +69,8 @@ constexpr int kTileUnits = 2, kItemUnits1 = 3, kItemUnits2 = 5;  // items of one
 // key tile, so that each of the CTAs between an item's first and last has a piece of it
 // (combine_kernel reads them all).
 constexpr int kMinUnits = kTileUnits;
+// Items of a sequence that one lane of the planner adds up; more take the whole warp.
+constexpr int kLaneItems = 16;
 // The planner keeps the units of so many sequences; it works those of more out twice.
 constexpr int kPlanSeqs = 1024;
 // Epilogue: an item of so many rows at most (one warp's) has its first finished slot put
@@ -187,11 +189,11 @@ __device__ __forceinline__ int items_of(const Geo& g, int nq) { return (nq + 2 *
 __device__ __forceinline__ long long head_units(const ExtendArgs& a, const Geo& g, const Seq& s, int lane) {
   const int np = items_of(g, s.nq);
   long long u = 0;
-  if (np <= 4) {
+  if (np <= kLaneItems) {
 #pragma unroll 1
     for (int p = 0; p < np; ++p) u += item_units(a, g, s, p);
   }
-  unsigned many = __ballot_sync(0xffffffffu, np > 4);
+  unsigned many = __ballot_sync(0xffffffffu, np > kLaneItems);
 #pragma unroll 1
   while (many) {
     const int src = __ffs(many) - 1;
@@ -738,25 +740,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto bit = [&](uint32_t i) { return (ph >> i) & 1u; };
       bool ok = true;
       auto free_tile = [&](uint64_t* empty, int g) { commit_elect(smem_u32(empty + g % NS)); };
-      // A place in the stream: piece, key tile, slot, the tile's number in the CTA.
+      // A place in the stream: piece, key tile, slot, the tile's number in the CTA; the key
+      // tiles [a, b) of its slot and [a2, b2) of the other one, the piece's last (exclusive).
+      // Kept in registers: a step reads them some ten times, and a dependent shared-memory
+      // read a time made the steps 1500 cycles longer.
       struct Step {
-        int i, j, t, g;
+        int i, j, t, g, a, b, a2, b2, j1;
+        bool single, fresh;  // fresh: the piece's first step
       };
       auto open_piece = [&](Step& at) {
         const Piece& p = pieces.at(at.i);
         at.j = p.j0;
+        at.j1 = p.j1;
         at.t = p.slot0;
         at.g = p.tile0;
+        at.single = p.single;
+        at.fresh = true;
+        at.a = p.first[at.t];
+        at.b = p.end[at.t];
+        at.a2 = p.first[at.t ^ 1];
+        at.b2 = p.end[at.t ^ 1];
       };
       // Is this the step's key tile's last step?  (Two-tile items: slot 1's.)
-      auto last_of_tile = [&](const Piece& p, const Step& at) { return p.single || at.t == 1; };
+      auto last_of_tile = [&](const Step& at) { return at.single || at.t == 1; };
+      // Does the step's slot have its key tile?
+      auto real = [&](const Step& at) { return at.j >= at.a && at.j < at.b; };
       // To the next step of the piece; false past its last.
-      auto advance = [&](const Piece& p, Step& at) {
-        const bool next_tile = last_of_tile(p, at);
+      auto advance = [&](Step& at) {
+        const int next_tile = last_of_tile(at) ? 1 : 0;
         at.t ^= 1;
         at.j += next_tile;
         at.g += next_tile;
-        return at.j < p.j1;
+        at.fresh = false;
+        const int a = at.a, b = at.b;
+        at.a = at.a2;
+        at.b = at.b2;
+        at.a2 = a;
+        at.b2 = b;
+        return at.j < at.j1;
       };
       auto k_landed = [&](int g) {
         return wait_bar(smem_u32(&sm.k_full[g % NS]), static_cast<uint32_t>((g / NS) & 1), abort_flag);
@@ -774,7 +795,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint4 bad = *reinterpret_cast<const uint4*>(sm.bad[g & 3]);
         return (bad.x | bad.y | bad.z | bad.w) != 0u;
       };
-      Step sc{0, 0, 0, 0}, oc{0, -1, 0, 0};  // the next S, the next PV (j = -1: its piece is to be opened)
+      Step sc{}, oc{};  // the next S, the next PV
+      bool o_open = false;  // oc's piece is open
       int ahead = 0;                         // steps that S is ahead of PV
       bool s_more = pieces.wait(0);
       if (s_more) open_piece(sc);
@@ -784,12 +806,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       while (ok && (s_more || ahead > 0)) {
         const bool do_o = ahead == 2 || !s_more || (hold && ahead == 1);
         const bool do_s = s_more && !(hold && ahead - do_o > 0);
-        if (do_o && oc.j < 0) open_piece(oc);
-        if (do_o && do_s && sc.i == oc.i && oc.t == 0) {
+        if (do_o && !o_open) {
+          open_piece(oc);
+          o_open = true;
+        }
+        if (do_o && do_s && sc.i == oc.i && oc.t == 0 && !oc.single) {
           // Inside a two-tile item, away from its edges: the same steps without their questions.
-          const Piece& p = pieces.at(oc.i);
-          const int end = p.single ? 0 : min(p.end[0], p.end[1]) - 2;
-          if (oc.j < end && oc.j > max(p.first[0], p.first[1])) {
+          const int end = min(oc.b, oc.b2) - 2;
+          if (oc.j < end && oc.j > max(oc.a, oc.a2)) {
             int g = oc.g;
             const int g_end = g + end - oc.j;
 #pragma unroll 1
@@ -819,9 +843,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (do_s) {
           // K and, for its first use, Q have landed: waited for ahead of the PV, so that the
           // two follow one another into the tensor pipe.
-          const Piece& p = pieces.at(sc.i);
-          if (sc.j == (p.single ? p.j0 : p.first[sc.t]) && sc.j < p.end[sc.t]) {
-            const int qs = p.single ? sc.i & 1 : sc.t;
+          if (sc.single ? sc.fresh : sc.j == sc.a && sc.j < sc.b) {
+            const int qs = sc.single ? sc.i & 1 : sc.t;
             ok = wait_bar(smem_u32(&sm.q_full[qs]), bit(Q_PH + qs), abort_flag);
             ph ^= 1u << (Q_PH + qs);
           }
@@ -829,16 +852,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
         }
         if (do_o) {
-          const Piece& p = pieces.at(oc.i);
           const int t = oc.t;
           const uint32_t v = tiles + kVOff + oc.g % NS * TILE_BYTES;
-          if (p.single || t == 0) {
+          if (oc.single || t == 0) {
             // V has landed.  Rows without a key of the item are kept out of the product: whole
             // steps of 16 keys are not issued (`steps`: first and end), the others' rows, and
             // those of blocks outside the pool, are cleared.
             ok = v_landed(oc.g);
             if (!ok) break;
-            const int lo = max(0, p.key_lo - oc.j * BN), hi = min(BN, p.key_hi - oc.j * BN);
+            int lo = 0, hi = BN;
+            if (oc.fresh || oc.j + 1 == oc.j1) {
+              const Piece& p = pieces.at(oc.i);
+              lo = max(0, p.key_lo - oc.j * BN);
+              hi = min(BN, p.key_hi - oc.j * BN);
+            }
             steps = make_int2(lo >> 4, (hi + 15) >> 4);
             const bool bad = any_bad(oc.g);
             if ((lo & 15) != 0 || (hi & 15) != 0 || bad) {
@@ -849,10 +876,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               __syncwarp();
             }
           }
-          if (oc.j >= p.first[t] && oc.j < p.end[t]) {
+          if (real(oc)) {
             // The slot's first PV of the item overwrites O_t (which the epilogue must have read
             // out), its last publishes it.
-            const bool first = oc.j == p.first[t], last = oc.j + (p.single ? 2 : 1) >= p.end[t];
+            const bool first = oc.j == oc.a, last = oc.j + (oc.single ? 2 : 1) >= oc.b;
             if (first && bit(O_USED + t)) {
               ok = wait_bar(smem_u32(&sm.o_free[t]), bit(O_PH + t), abort_flag);
               ph ^= 1u << (O_PH + t);
@@ -871,25 +898,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               ph |= 1u << (O_USED + t);
             }
           }
-          if (last_of_tile(p, oc)) free_tile(sm.v_empty, oc.g);
+          if (last_of_tile(oc)) free_tile(sm.v_empty, oc.g);
           --ahead;
-          if (!advance(p, oc)) {
+          if (!advance(oc)) {
             pieces.release(oc.i++, lane);
-            oc.j = -1;
+            o_open = false;
           }
         }
         if (do_s) {
-          const Piece& p = pieces.at(sc.i);
-          if (sc.j >= p.first[sc.t] && sc.j < p.end[sc.t]) {
-            const int qs = p.single ? sc.i & 1 : sc.t;
+          if (real(sc)) {
+            const int qs = sc.single ? sc.i & 1 : sc.t;
             issue_qk<T>(tmem + 128 * sc.t, tiles + qs * TILE_BYTES, tiles + kKOff + sc.g % NS * TILE_BYTES);
             commit_elect(smem_u32(&sm.s_full[sc.t]));
-            if (sc.j + 1 == (p.single ? p.j1 : p.end[sc.t])) commit_elect(smem_u32(&sm.q_empty[qs]));
+            if (sc.j + 1 == sc.b) commit_elect(smem_u32(&sm.q_empty[qs]));
           }
-          if (last_of_tile(p, sc)) free_tile(sm.k_empty, sc.g);
+          if (last_of_tile(sc)) free_tile(sm.k_empty, sc.g);
           ++ahead;
           hold = false;
-          if (!advance(p, sc)) {
+          if (!advance(sc)) {
             const int t = sc.t ^ 1;  // the slot of the step just issued
             ++sc.i;
             s_more = pieces.wait(sc.i);
