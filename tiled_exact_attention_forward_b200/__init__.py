@@ -30,6 +30,7 @@ The ring (context-parallel) forward over torch.distributed ranks sits in
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -150,14 +151,14 @@ def _check(status: int, where: str):
         raise FAError(status, where)
 
 
+_DTYPE_CODES = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16, torch.float32: FA_FP32}
+
+
 def _dtype_code(dt: torch.dtype) -> int:
-    if dt == torch.bfloat16:
-        return FA_BF16
-    if dt == torch.float16:
-        return FA_FP16
-    if dt == torch.float32:
-        return FA_FP32
-    raise TypeError(f"unsupported dtype {dt}: use torch.bfloat16, torch.float16 or torch.float32")
+    code = _DTYPE_CODES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}: use torch.bfloat16, torch.float16 or torch.float32")
+    return code
 
 
 def _need_cuda(*ts):
@@ -506,7 +507,7 @@ def _addr(t):
 
 
 def _need_int32(name, t, shape):
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+    if t.shape != shape or t.dtype != torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
 
 
@@ -547,9 +548,10 @@ def _rotation_args(dtype, q_weight, k_weight, rope, eps, d):
     """(rot, max_pos, eps for the C ABI, weight dtype code) of a norm and rotation."""
     rot = max_pos = 0
     if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+        shape = rope.shape
+        if len(shape) != 2 or rope.dtype != torch.float32 or not rope.is_contiguous():
             raise ValueError("rope must be a contiguous float32 tensor [positions, rot]: rot/2 cosines, rot/2 sines")
-        max_pos, rot = rope.shape
+        max_pos, rot = shape
         if rot == 0 or rot % 16 or rot > d:
             raise ValueError("rope's second dimension must be a multiple of 16 up to the head dimension")
     if eps is None:
@@ -560,14 +562,14 @@ def _rotation_args(dtype, q_weight, k_weight, rope, eps, d):
         raise ValueError("eps must be >= 0 (None: no norm)")
     wdt = None
     for w in (q_weight, k_weight):
-        if w is None:
-            continue
-        if w.shape != (d,) or not w.is_contiguous():
-            raise ValueError("weights must be contiguous tensors of the head dimension")
-        if w.dtype != (wdt or w.dtype) or (w.dtype != dtype and w.dtype != torch.float32):
-            raise ValueError("weights must share one dtype: the tensors' or float32")
-        wdt = w.dtype
-    return rot, max_pos, float(eps), _dtype_code(wdt or dtype)
+        if w is not None:
+            t = w.dtype
+            if w.shape != (d,) or not w.is_contiguous():
+                raise ValueError("weights must be contiguous tensors of the head dimension")
+            if (t != dtype and t != torch.float32) or (wdt is not None and t != wdt):
+                raise ValueError("weights must share one dtype: the tensors' or float32")
+            wdt = t
+    return rot, max_pos, float(eps), _dtype_code(dtype if wdt is None else wdt)
 
 
 def _position_stride(positions, B, N):
@@ -627,6 +629,7 @@ def norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=None
     return (q_out, k_out) if k is not None else q_out
 
 
+@functools.lru_cache(maxsize=None)
 def norm_rope_backward_workspace_size(d) -> int:
     return int(_lib().fa_norm_rope_backward_workspace_size(d))
 
@@ -664,7 +667,7 @@ def norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope=
     ws_bytes = 0
     if dqw is not None or dkw is not None:
         if workspace is None:
-            workspace = torch.empty(norm_rope_backward_workspace_size(d), dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty((norm_rope_backward_workspace_size(d),), dtype=torch.uint8)
         ws_bytes = workspace.numel() * workspace.element_size()
     _launch(_lib().fa_norm_rope_backward, "fa_norm_rope_backward", device, q.data_ptr(), _addr(k), dq_out.data_ptr(),
             _addr(dk_out), dq.data_ptr(), _addr(dk), strides, _addr(q_weight), _addr(k_weight), _addr(dqw), _addr(dkw),
@@ -772,6 +775,7 @@ def append_paged(k, v, kpool, vpool, block_table, seqlens, cu_tokens=None, rope=
     return q_out
 
 
+@functools.lru_cache(maxsize=4096)
 def extend_paged_workspace_size(T, Hq, Hkv, d) -> int:
     return int(_lib().fa_extend_paged_workspace_size(T, Hq, Hkv, d))
 

@@ -30,6 +30,8 @@
 // block's unused tail, a skipped block) stay out of the product: steps of 16 keys
 // without a key are not issued, other such rows are zeroed in shared memory before
 // the MMA, since their weights are zero but 0 * NaN is not.
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -1323,11 +1325,17 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
       !make_tmap_3d_half(&tv, a.vpool, pd, ps, pb, a.f16))
     return cudaErrorInvalidValue;
   auto kernel = a.f16 ? extend_kernel<F16> : extend_kernel<Bf16>;
-  // With fewer registers than the split draws on, setmaxnreg.inc would wait forever.
-  cudaFuncAttributes fattr{};
-  cudaError_t e = cudaFuncGetAttributes(&fattr, reinterpret_cast<const void*>(kernel));
-  if (e != cudaSuccess) return e;
-  if (fattr.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+  // With fewer registers than the split draws on, setmaxnreg.inc would wait forever.  One
+  // build has one answer, so it is asked for once.
+  static std::atomic<bool> fits[2];
+  cudaError_t e = cudaSuccess;
+  if (!fits[a.f16 != 0].load(std::memory_order_relaxed)) {
+    cudaFuncAttributes fattr{};
+    e = cudaFuncGetAttributes(&fattr, reinterpret_cast<const void*>(kernel));
+    if (e != cudaSuccess) return e;
+    if (fattr.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    fits[a.f16 != 0].store(true, std::memory_order_relaxed);
+  }
   e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmemBytes);
   if (e != cudaSuccess) return e;
   int sms = 0;
