@@ -1251,58 +1251,81 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 // Joins the partial results of an item that several CTAs share: with lse_s of piece s,
-// lse = ln sum exp(lse_s), o = sum exp(lse_s - lse) o_s.  One warp per row; block x
-// looks at the item that begins in CTA x and ends in a later one, if there is one.
-constexpr int CB_WARPS = 8;
+// lse = ln sum exp(lse_s), o = sum exp(lse_s - lse) o_s, in the order of the pieces.  Block
+// x looks at the item that begins in CTA x and ends in a later one, if there is one.  A
+// warp takes four rows at a time, eight lanes reading a row's logsumexps, all lanes its o,
+// so that four rows' loads are in flight (one row a warp: 22.6 us on the 2048-token piece).
+constexpr int CB_WARPS = 8, CB_ROWS = 4;
 template <class T>
 __global__ void __launch_bounds__(CB_WARPS * 32) combine_kernel(const __grid_constant__ ExtendArgs args) {
   wait_for_previous_kernel();
   const ExtendDesc d = args.desc[blockIdx.x];
   if (d.last < 0) return;
   const int lane = threadIdx.x & 31;
-  const int G = args.Hq / args.Hkv, tpt = BM / G;
+  const int G = args.Hq / args.Hkv, tpt = BM / G, rows = d.ntok * G;
   const int first = blockIdx.x, pieces = d.last - first + 1;
-  for (int r = blockIdx.y * CB_WARPS + (threadIdx.x >> 5); r < d.ntok * G; r += gridDim.y * CB_WARPS) {
-    const int tok = r / G, head = r - tok * G;
-    const int t = tok >= tpt ? 1 : 0;
-    const int srow = t * BM + r - t * tpt * G;  // the row's place in a slot
-    auto row_of = [&](int s) {
-      return static_cast<long long>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * args.slot_rows + srow;
-    };
+  const float nan = __uint_as_float(0x7fc00000u);
+  // With no more rows than a block has warps each warp takes one.
+  const int nk = rows <= CB_WARPS ? 1 : CB_ROWS;
+  for (int r0 = (blockIdx.y * CB_WARPS + (threadIdx.x >> 5)) * nk; r0 < rows; r0 += gridDim.y * CB_WARPS * nk) {
+    // This lane's row of the four: its place in a slot and in the output.
+    const int mine = nk == 1 ? 0 : lane >> 3;
+    const int r = min(r0 + mine, rows - 1), tok = r / G, t = tok >= tpt ? 1 : 0;
+    const int srow = t * BM + r - t * tpt * G;
+    const long long out = static_cast<long long>(d.tok0 + tok) * args.Hq + d.kvh * G + r - tok * G;
+    // Piece s of the item lies in this slot of the workspace.
+    auto slot_at = [&](int s) { return static_cast<long long>(s == 0 ? 2 * first + 1 : 2 * (first + s)) * args.slot_rows; };
     float M = -INFINITY;
-    for (int s = lane; s < pieces; s += 32) {
-      const float v = args.ws_lse[row_of(s)];
-      M = M != M || v != v ? __uint_as_float(0x7fc00000u) : fmaxf(M, v);
+    for (int s = lane & 7; s < pieces; s += 8) {
+      const float v = args.ws_lse[slot_at(s) + srow];
+      M = M != M || v != v ? nan : fmaxf(M, v);
     }
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) {
+    for (int x = 4; x > 0; x >>= 1) {
       const float v = __shfl_xor_sync(0xffffffffu, M, x);
-      M = M != M || v != v ? __uint_as_float(0x7fc00000u) : fmaxf(M, v);
+      M = M != M || v != v ? nan : fmaxf(M, v);
     }
-    float W = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M != -INFINITY) {
-      for (int s0 = 0; s0 < pieces; s0 += 32) {
-        const float w_l = s0 + lane < pieces ? __expf(args.ws_lse[row_of(s0 + lane)] - M) : 0.f;
-        const int n = min(32, pieces - s0);
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-          const float w = __shfl_sync(0xffffffffu, w_l, i);
-          if (w == 0.f) continue;  // a piece without a visible key wrote no o
-          const float4 v = *reinterpret_cast<const float4*>(args.ws_o + row_of(s0 + i) * D + lane * 4);
-          W += w;
-          acc.x = fmaf(w, v.x, acc.x);
-          acc.y = fmaf(w, v.y, acc.y);
-          acc.z = fmaf(w, v.z, acc.z);
-          acc.w = fmaf(w, v.w, acc.w);
+    float W = 0.f;  // this lane's row's
+    float4 acc[CB_ROWS];
+#pragma unroll
+    for (int k = 0; k < CB_ROWS; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < pieces; s0 += 8) {
+      const int s = s0 + (lane & 7);
+      const float w_l = s < pieces && M != -INFINITY ? __expf(args.ws_lse[slot_at(s) + srow] - M) : 0.f;
+      const int n = min(8, pieces - s0);
+#pragma unroll 2
+      for (int i = 0; i < n; ++i) {
+        const float* o = args.ws_o + slot_at(s0 + i) * D + lane * 4;
+        W += __shfl_sync(0xffffffffu, w_l, (lane & 24) + i);
+        float w[CB_ROWS];
+        float4 v[CB_ROWS];
+#pragma unroll
+        for (int k = 0; k < CB_ROWS; ++k) {
+          w[k] = __shfl_sync(0xffffffffu, w_l, 8 * k + i);
+          const int row = __shfl_sync(0xffffffffu, srow, 8 * k);
+          // A piece without a visible key wrote no o.
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < nk && w[k] != 0.f) v[k] = *reinterpret_cast<const float4*>(o + row * D);
+        }
+#pragma unroll
+        for (int k = 0; k < CB_ROWS; ++k) {
+          acc[k].x = fmaf(w[k], v[k].x, acc[k].x);
+          acc[k].y = fmaf(w[k], v[k].y, acc[k].y);
+          acc[k].z = fmaf(w[k], v[k].z, acc[k].z);
+          acc[k].w = fmaf(w[k], v[k].w, acc[k].w);
         }
       }
     }
-    const float inv = W == 0.f ? 0.f : 1.f / W;  // a NaN logsumexp makes the row NaN
-    const long long out = static_cast<long long>(d.tok0 + tok) * args.Hq + d.kvh * G + head;
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.o) + out * D + lane * 4) =
-        make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
-    if (lane == 0 && args.lse != nullptr) args.lse[out] = W == 0.f ? -INFINITY : M + logf(W);
+#pragma unroll
+    for (int k = 0; k < CB_ROWS; ++k) {
+      const float Wk = __shfl_sync(0xffffffffu, W, 8 * k);
+      const long long at = __shfl_sync(0xffffffffu, out, 8 * k);
+      const float inv = Wk == 0.f ? 0.f : 1.f / Wk;  // a NaN logsumexp makes the row NaN
+      if (k < nk && r0 + k < rows)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.o) + at * D + lane * 4) =
+            make_uint2(pack2<T>(acc[k].x * inv, acc[k].y * inv), pack2<T>(acc[k].z * inv, acc[k].w * inv));
+    }
+    if ((lane & 7) == 0 && (lane >> 3) < nk && r0 + mine < rows && args.lse != nullptr) args.lse[out] = W == 0.f ? -INFINITY : M + logf(W);
   }
 }
 
@@ -1344,7 +1367,7 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(sms < kExtendMaxCtas ? sms : kExtendMaxCtas);
   e = launch_dependent(kernel, dim3(grid), dim3(NUM_THREADS), kSmemBytes, stream, tq, tk, tv, a, box);
   if (e != cudaSuccess) return e;
-  const dim3 cgrid(grid, (a.slot_rows + CB_WARPS * 4 - 1) / (CB_WARPS * 4));
+  const dim3 cgrid(grid, (a.slot_rows + CB_WARPS * CB_ROWS - 1) / (CB_WARPS * CB_ROWS));
   return launch_dependent(a.f16 ? combine_kernel<F16> : combine_kernel<Bf16>, cgrid, dim3(CB_WARPS * 32), 0, stream, a);
 }
 
