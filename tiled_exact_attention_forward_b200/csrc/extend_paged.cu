@@ -280,8 +280,10 @@ __device__ __forceinline__ long long div_up(long long a, unsigned b) {
   return (static_cast<long long>(q) << 16) + ((hi - q * b) << 16 | lo) / b;
 }
 // This CTA's run, found by one warp, 32 sequences at a time.  The units of the first
-// kPlanSeqs are kept for the second walk.
-__device__ __forceinline__ void find_run(const ExtendArgs& a, const Geo& g, Ctl& sm, int lane) {
+// kPlanSeqs are kept for the second walk.  Out of line, and called ahead of the register
+// split: its code runs once and stays away from the roles' loops.
+__device__ __noinline__ void find_run(const ExtendArgs& a, Ctl& sm, int lane) {
+  const Geo g{a.Hq / a.Hkv, BM / (a.Hq / a.Hkv)};
   long long total = 0, length = 0, begin = 0, before = 0;
 #pragma unroll 1
   for (int walk = 0; walk < 2; ++walk) {
@@ -413,7 +415,7 @@ __device__ __forceinline__ void zero_v_rows(uint32_t v_addr, int r0, int r1, int
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + r * 128), "r"(0u) : "memory");
 }
 // Zeroes the rows of blocks outside the pool (bit r of `bad`).
-__device__ __noinline__ void zero_bad_rows(uint32_t v_addr, const uint32_t* bad, int lane) {
+__device__ __forceinline__ void zero_bad_rows(uint32_t v_addr, const uint32_t* bad, int lane) {
 #pragma unroll 1
   for (int r = 0; r < BN; ++r)
     if (bad[r >> 5] >> (r & 31) & 1u) zero_v_rows(v_addr, r, r + 1, lane);
@@ -454,6 +456,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // Everything before this overlaps the end of the kernel ahead in the stream.
   wait_for_previous_kernel();
   let_next_kernel_start();
+  if (warp == PLAN_WARP) find_run(args, sm, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -472,7 +475,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // Finds the run, walks it item by item, hands out its pieces and loads their Q tiles.
       const Geo geo = geometry();
       const uint32_t tiles = tiles_base();
-      find_run(args, geo, sm, lane);
       ExtendDesc open{0, 0, 0, -1};  // the item that begins here and ends in another CTA
       int ip = 0, tile0 = 0, slot0 = 0;  // pieces handed out, their key tiles, the next slot in turn
       int iq = 0;                    // pieces whose Q is on its way
