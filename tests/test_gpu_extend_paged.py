@@ -286,6 +286,83 @@ def test_two_streams_at_once():
         assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
 
 
+def test_pool_offsets_past_32_bits():
+    """Pools of more than 2^31 elements each: blocks at their far ends are read at their places."""
+    Hkv, block = 8, 4096
+    num = (1 << 31) // (block * Hkv * 128) + 3
+    g = torch.Generator().manual_seed(27)
+    small = [torch.randn(2, Hkv, block, 128, generator=g).to(BF16) for _ in range(2)]
+    q = torch.randn(3, Hkv, 128, generator=g).to(BF16)
+    kp, vp = (torch.zeros(num, Hkv, block, 128, dtype=BF16, device="cuda") for _ in range(2))
+    for pool, rows in ((kp, small[0]), (vp, small[1])):
+        pool[num - 1], pool[num - 2] = rows[0].cuda(), rows[1].cuda()
+    table = torch.tensor([[num - 1, num - 2]], dtype=torch.int32)
+    lens, cu = torch.tensor([5000], dtype=torch.int32), torch.tensor([0, 3], dtype=torch.int32)
+    o, lse = fa.extend_paged(q.cuda(), kp, vp, table.cuda(), lens.cuda(), cu_tokens=cu.cuda())
+    assert fa.device_status() == fa.FA_OK
+    o_ref, l_ref, ob, lb = attend(q, *small, torch.tensor([[0, 1]], dtype=torch.int32), cu, lens)
+    assert_within(o, o_ref, ob, "o")
+    assert_within(lse, l_ref, lb, "lse")
+
+
+def test_tokens_outside_every_sequence_and_shared_blocks():
+    """cu_tokens that begins past 0, sequences that share their first blocks, the same block twice."""
+    q, kp, vp, table, cu, lens = make([4, 6, 70], [100, 120, 200], 4, 2, 16, BF16, seed=28, extra=9)
+    cu = cu + 5
+    table[1, :6] = table[0, :6]
+    table[2, 3] = table[2, 7]
+    out = torch.full(q.shape, 7.0, dtype=BF16, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    fa.extend_paged(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), lens.cuda(), cu_tokens=cu.cuda(), out=out, lse=lse)
+    assert fa.device_status() == fa.FA_OK
+    o_ref, l_ref, ob, lb = attend(q, kp, vp, table, cu, lens)
+    assert_within(out[5:85], o_ref[5:85], ob[5:85], "o")
+    assert_within(lse[5:85], l_ref[5:85], lb[5:85], "lse")
+    assert (out[:5] == 7.0).all() and (out[85:] == 7.0).all() and (lse[85:] == 7.0).all()
+
+
+def test_bad_token_bounds_stay_inside_the_batch():
+    """cu_tokens below 0 and past T are clamped: nothing outside the outputs is touched."""
+    q, kp, vp, table, cu, lens = make([3, 4], [50, 60], 4, 2, 16, BF16, seed=29)
+    cu = torch.tensor([-5, 3, 1000], dtype=torch.int32)
+    lens = torch.tensor([50, 60], dtype=torch.int32)
+    guard = torch.full((3, 7, 4, 128), 7.0, dtype=BF16, device="cuda")
+    fa.extend_paged(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), lens.cuda(), cu_tokens=cu.cuda(), out=guard[1])
+    assert fa.device_status() == fa.FA_OK
+    o_ref, _, ob, _ = attend(q, kp, vp, table, torch.tensor([0, 3, 7]), lens)
+    assert_within(guard[1], o_ref, ob, "o")
+    assert (guard[0] == 7.0).all() and (guard[2] == 7.0).all()
+
+
+def test_workspace_of_another_call_and_of_stale_bits():
+    """The workspace's contents do not matter: NaN bits, or another call's partial results."""
+    a = make([1, 200], [9000, 3000], 8, 2, 16, BF16, seed=30)
+    b = make([130, 3], [700, 20000], 8, 2, 16, BF16, seed=32)
+    size = fa.extend_paged_workspace_size(300, 8, 2, 128)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    run = lambda c, **kw: fa.extend_paged(*(t.cuda() for t in (c[0], c[1], c[2], c[3], c[5], c[4])), **kw)  # noqa: E731
+    for c in (a, b, a):
+        want, got = run(c), run(c, workspace=ws)
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+def test_right_after_the_kernel_that_writes_its_inputs():
+    """The launch overlaps the end of the kernel ahead of it, but reads nothing before that is done."""
+    q, kp, vp, table, cu, lens = make([1, 1, 90], [2000, 30, 400], 8, 2, 16, BF16, seed=33)
+    dev = [t.cuda() for t in (q, kp, vp, table, lens, cu)]
+    want = fa.extend_paged(*dev)
+    work = [torch.zeros_like(t) for t in dev]
+    big = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        for t in work:
+            t.zero_()
+        big.fill_(1)  # keeps the stream busy while the launches below queue up
+        for t, s in zip(work, dev):
+            t.copy_(s)
+        got = fa.extend_paged(*work)
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
 def test_a_serving_run():
     """Prompt pieces and single tokens of two sequences through append_paged, extend_paged and
     decode_paged, against the causal attention of the whole sequences."""
