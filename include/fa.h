@@ -267,7 +267,8 @@ FA_API fa_status fa_backward(const void* q, const void* k, const void* v, const 
  *     r = 1 / sqrt(mean(x^2) + eps),  y = x r w,  z = R(p) y
  * for every row x of d elements, R(p) turning pairs of the first `rot` elements by
  * the angles of position p: (a, b) -> (a cos - b sin, b cos + a sin).  float32
- * arithmetic, one rounding to the output's type.
+ * arithmetic, one rounding to the output's type.  (A row whose squares sum past
+ * float32's range has r = 0 and comes out as zeros.)
  *
  *   q, k       : [B][Hq][N][d] and [B][Hk][N][d] (dtype FA_BF16, FA_FP16 or
  *                FA_FP32; d = 64 or 128) at free strides, each row contiguous.
@@ -353,6 +354,8 @@ FA_API fa_status fa_norm_rope_backward(const void* q, const void* k, const void*
  *                 that is contiguous); both NULL: no queries.
  *   q_weight, k_weight, rope, rot, max_pos, eps, interleaved, weight_dtype: as
  *                 fa_norm_rope (without norm and rotation the keys are copied).
+ * Two new tokens must not share a place (sequences may share blocks of earlier
+ * tokens): which of them is kept is not defined.
  * A token whose position lies outside [0, max_blocks * block_size) or the table,
  * or whose block id lies outside [0, num_blocks), is not written (its q_out row
  * comes out NaN where it would be turned) and FA_ERR_INVALID is recorded for

@@ -138,6 +138,13 @@ def test_rows_of_zeros_and_large_values():
     check(q, k, dq, dk, qw, kw, rope, 1e-6, False, table=rope)
 
 
+@pytest.mark.parametrize("size,eps", [(1e15, 1e-6), (1e-15, 0.0), (1e-3, 0.0)])
+def test_rows_far_from_one(size, eps):
+    """1/|x| cubed leaves float32's range at the first two sizes; the gradients do not."""
+    q, k, dq, dk, qw, kw, rope = make(1, 2, 2, 8, 128, 128, FP32, seed=19)
+    check(q * size, k * size, dq, dk, qw, kw, rope, eps, False, table=rope)
+
+
 def test_non_finite_rows_stay_in_their_rows():
     q, k, dq, dk, qw, kw, rope = make(1, 4, 2, 20, 128, 128, BF16, seed=10)
     want, _ = fa.norm_rope(q.cuda(), k.cuda(), qw.cuda(), kw.cuda(), rope.cuda())
@@ -229,6 +236,39 @@ def test_broadcast_head_gets_its_gradient():
     dx, b, _, _ = norm_rotate_grads(k1.detach().cpu().expand(1, 4, 30, 64), dk, None, rope, 1e-6, False)
     # torch adds the four float32 gradients: three roundings of partial sums more.
     assert_within(k1.grad, dx.sum(1, keepdim=True), (b + 4 * 2.0 ** -24 * dx.abs()).sum(1, keepdim=True), "shared head")
+
+
+@pytest.mark.parametrize("how", ["sum", "narrow", "offset", "turned"])
+def test_gradients_as_autograd_lays_them_out(how):
+    """Expanded, sliced, misaligned and transposed gradients of the outputs."""
+    x = torch.randn(2, 3, 20, 64, generator=torch.Generator().manual_seed(20)).to(BF16).cuda()
+    rope = rope_table(20, 64).cuda()
+    w = torch.ones(64, dtype=BF16, device="cuda")
+    leaf, lw = x.clone().requires_grad_(), w.clone().requires_grad_()
+    y = fa.qk_norm_rope(leaf, None, lw, None, rope)
+    c = torch.randn(2, 3, 20, 64, generator=torch.Generator().manual_seed(21)).to(BF16).cuda()
+    if how == "sum":
+        g = torch.ones_like(x)
+        y.sum().backward()
+    elif how == "narrow":  # rows 65 elements apart
+        g = c
+        torch.cat([y, y.new_zeros(2, 3, 20, 1)], -1).backward(torch.cat([c, c[..., :1]], -1))
+    elif how == "offset":  # rows that begin 2 bytes past a boundary
+        g = c
+        y.backward(torch.cat([c.new_zeros(1), c.flatten()])[1:].view_as(c))
+    else:
+        g = c
+        y.transpose(2, 3).backward(c.transpose(2, 3).contiguous())
+    want = fa.norm_rope_backward(x, None, g, None, w, None, rope)
+    assert torch.equal(leaf.grad, want[0]) and torch.equal(lw.grad, want[2])
+
+
+def test_second_derivatives_are_refused():
+    x = torch.randn(1, 1, 4, 64, device="cuda").requires_grad_()
+    y = fa.qk_norm_rope(x, rope=rope_table(4, 64).cuda())
+    (g,) = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
 
 
 def test_captured_and_replayed():

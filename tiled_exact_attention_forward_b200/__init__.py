@@ -544,6 +544,15 @@ def _grad_like(t):
     return g if g.stride(-1) == 1 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
+def _readable(g):
+    """g, or a copy where the kernels cannot read it in place (its layout is what autograd made of it)."""
+    e = g.element_size()
+    if g.stride(-1) == 1 and g.data_ptr() % 16 == 0:
+        if all(n < 2 or st * e % 16 == 0 for n, st in zip(g.shape[:-1], g.stride())):
+            return g
+    return g.clone(memory_format=torch.contiguous_format)
+
+
 def _rotation_args(dtype, q_weight, k_weight, rope, eps, d):
     """(rot, max_pos, eps for the C ABI, weight dtype code) of a norm and rotation."""
     rot = max_pos = 0
@@ -686,18 +695,18 @@ class _QKNormRope(torch.autograd.Function):
         return norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, gq, gk=None):
         q, k, q_weight, k_weight, rope, positions = ctx.saved_tensors
-        gq = gq if gq.stride(-1) == 1 else gq.contiguous()
-        if gk is not None and gk.stride(-1) != 1:
-            gk = gk.contiguous()
-        dq, dk, dqw, dkw = norm_rope_backward(q, k, gq, gk, q_weight, k_weight, rope, positions, *ctx.how)
+        dq, dk, dqw, dkw = norm_rope_backward(q, k, _readable(gq), None if gk is None else _readable(gk), q_weight,
+                                              k_weight, rope, positions, *ctx.how)
         return dq, dk, dqw, dkw, None, None, None, None
 
 
 def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6,
                  interleaved: bool = False):
-    """norm_rope with autograd: gradients for q, k and the weights (rope and positions have none).
+    """norm_rope with autograd: gradients for q, k and the weights (rope and positions have none;
+    no second derivatives).
 
     The step before ``attention``: q, k = qk_norm_rope(q, k, ...); o = attention(q, k, v, causal=True).
     To capture forward and backward into a CUDA graph, drop every eager autograd graph of the

@@ -161,7 +161,9 @@ __global__ void __launch_bounds__(THREADS)
         const float ss = row_sum<L>(dot(xv, xv)), ux = row_sum<L>(dot(gx, w));
         // A dead row's r is 1 / sqrt(eps), infinite for eps = 0: kept out of dw.
         const float r = live && h < heads ? rsqrt_row(ss * (1.f / D) + a.eps) : 0.f;
-        const uint64_t r2 = f2_both(r), c2 = f2_both(-r * r * r * (ux * (1.f / D)));
+        // (r ux) first: r^3 leaves float32's range where the product does not (|x| near 1e13 or,
+        // with eps = 0, 1e-13).
+        const uint64_t r2 = f2_both(r), c2 = f2_both(-(r * ux) * (1.f / D) * r * r);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           dw[e] = f2_fma(gx.p[e], r2, dw[e]);
