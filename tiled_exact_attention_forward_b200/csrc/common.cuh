@@ -402,14 +402,6 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// ---------------------------------------------------------------- dependent launches
-// A kernel launched as dependent (launch_dependent, kernels.h) may start before the one
-// ahead of it in the stream is done: it waits here, before it reads anything of that one's,
-// until that one is complete and its writes are visible.
-__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the next kernel start as soon as every CTA of this one has got here.
-__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ---------------------------------------------------------------- math
 // 2^x on the special-function unit (approximate, flushes denormals; 2^-inf = 0).
 __device__ __forceinline__ float ex2_approx(float x) {

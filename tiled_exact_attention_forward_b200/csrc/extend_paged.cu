@@ -30,9 +30,24 @@
 // block's unused tail, a skipped block) stay out of the product: steps of 16 keys
 // without a key are not issued, other such rows are zeroed in shared memory before
 // the MMA, since their weights are zero but 0 * NaN is not.
+//
+// What bounds it, and what it measured (device time):
+//   2048 tokens of a prompt at 14336 .. 16383, 32 heads over 8: the tensor cores through
+//     the S -> softmax -> PV chain of a two-tile item, as in fwd_tc.cu; 422 us, 1220 TFLOP/s;
+//   64 single tokens, 512 .. 8192 keys, 32 heads over 8: the cache's bytes; 199 us,
+//     5.7 TB/s (87 % of the copy rate): a CTA's share is some 120 key tiles of a few items,
+//     and an item's edges (Q, first S, last PV, epilogue) cost as much as one or two tiles;
+//   24 x 5 tokens, 100 .. 4000 keys, 16 heads over 16: 93 us, 5.1 TB/s (78 %), shorter items;
+//   17 ragged pieces under a window of 1024: 98 us, 500 TFLOP/s: half the key tiles are
+//     partly masked, and some 35 units a CTA leave little to level out between CTAs;
+//   one token over 512 keys: 14.1 us: launch, planning, four key tiles' latency, the join.
+// The kernel's text is kept near 90 KB with single issue sites and loops that are not
+// unrolled: at 225 KB the sixteen warps' roles displaced one another in the instruction cache.
 #include <atomic>
 
+#include "cache_ops.h"
 #include "common.cuh"
+#include "dependent.cuh"
 #include "kernels.h"
 
 namespace fa {
@@ -370,8 +385,8 @@ __device__ __forceinline__ void load_o16(uint32_t tO, uint32_t tO1, bool both, b
   for (int e = 0; e < 16; ++e) o[e] = none ? 0.f : o[e];
 }
 
-// The bounded wait of common.cuh for a whole warp, in fewer instructions: there are some
-// thirty waits here.  (A suspend-time hint on try_wait, to leave the issue slots to the
+// The bounded wait of common.cuh for a whole warp, in fewer instructions: there are more
+// than a dozen waits here.  (A suspend-time hint on try_wait, to leave the issue slots to the
 // softmax warps, measured 3 % slower.)
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   bool ok = true;
@@ -1256,7 +1271,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // lse = ln sum exp(lse_s), o = sum exp(lse_s - lse) o_s, in the order of the pieces.  Block
 // x looks at the item that begins in CTA x and ends in a later one, if there is one.  A
 // warp takes four rows at a time, eight lanes reading a row's logsumexps, all lanes its o,
-// so that four rows' loads are in flight (one row a warp: 22.6 us on the 2048-token piece).
+// so that four rows' loads are in flight.  Bound by the latency of those loads, the partials
+// being in L2: 17.4 us after the 2048-token piece with cold caches (one row a warp: 22.6 us).
 constexpr int CB_WARPS = 8, CB_ROWS = 4;
 template <class T>
 __global__ void __launch_bounds__(CB_WARPS * 32) combine_kernel(const __grid_constant__ ExtendArgs args) {

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/fa.h"
+#include "cache_ops.h"
 #include "common.cuh"
 #include "kernels.h"
 

@@ -6,6 +6,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "cache_ops.h"
 #include "common.cuh"
 #include "kernels.h"
 

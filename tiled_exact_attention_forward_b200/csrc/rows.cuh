@@ -19,7 +19,6 @@
 #pragma once
 
 #include "common.cuh"
-#include "kernels.h"
 
 namespace fa {
 namespace rows {
