@@ -388,7 +388,7 @@ __device__ __forceinline__ void load_o16(uint32_t tO, uint32_t tO1, bool both, b
 // The bounded wait of common.cuh for a whole warp, in fewer instructions: there are more
 // than a dozen waits here.  (A suspend-time hint on try_wait, to leave the issue slots to the
 // softmax warps, measured 3 % slower.)
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   bool ok = true;
   const unsigned t0 = static_cast<unsigned>(clock());
 #pragma unroll 1
@@ -402,6 +402,17 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   }
   return __all_sync(0xffffffffu, ok);
 }
+__device__ __noinline__ bool wait_out_of_line(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return wait_inline(bar, parity, abort_flag);
+}
+// One try in line, the loop in one place for all: the MMA warp's steps are a chain of such
+// waits, most of them over already (5 drafted tokens 94 -> 90 us, ragged window 99 -> 95, 64
+// single tokens 200 -> 195).  The softmax warps, whose registers a call does not fit, take
+// wait_inline (a try ahead of its loop gained them nothing).
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_out_of_line(bar, parity, abort_flag);
+}
 
 // A warp's view of the planner's ring of pieces.  Pieces stay in shared memory until the
 // warp releases them: what a role needs of one now and then is read there, since a
@@ -413,8 +424,10 @@ struct Pieces {
   volatile int* abort_flag;
   __device__ __forceinline__ const Piece& at(int i) const { return sm->piece[i % NP]; }
   // Waits for piece i; false at the end (or when the CTA gives up).
+  template <bool INLINE = false>
   __device__ __forceinline__ bool wait(int i) const {
-    return wait_bar(smem_u32(&sm->piece_full[i % NP]), (i / NP) & 1, abort_flag) && !at(i).stop;
+    const uint32_t bar = smem_u32(&sm->piece_full[i % NP]), parity = (i / NP) & 1;
+    return (INLINE ? wait_inline(bar, parity, abort_flag) : wait_bar(bar, parity, abort_flag)) && !at(i).stop;
   }
   __device__ __forceinline__ void release(int i, int lane) const {
     __syncwarp();
@@ -1117,7 +1130,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t ph = ST_PH;
     bool ok = true;
 #pragma unroll 1
-    for (int ip = 0; ok && pieces.wait(ip); ++ip) {
+    for (int ip = 0; ok && pieces.wait<true>(ip); ++ip) {
       // Keys that this row sees, [row_lo, row_hi), and that every row of the tile sees,
       // [all_lo, all_hi): key tiles inside the latter need no mask.
       int row_lo, row_hi, all_lo, all_hi;
@@ -1144,7 +1157,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool nan_row = false, begun = false;
 #pragma unroll 1
       for (; j < end; j += step) {
-        ok = wait_bar(smem_u32(&sm.s_full[t]), ph & S_PH, abort_flag);
+        ok = wait_inline(smem_u32(&sm.s_full[t]), ph & S_PH, abort_flag);
         if (!ok) break;
         ph ^= S_PH;
         if (!busy) {
@@ -1249,7 +1262,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       if (!ok) break;
-      if (ph & ST_ANY) ok = wait_bar(smem_u32(&sm.st_empty[t]), (ph & ST_PH) != 0u, abort_flag);
+      if (ph & ST_ANY) ok = wait_inline(smem_u32(&sm.st_empty[t]), (ph & ST_PH) != 0u, abort_flag);
       if (!ok) break;
       ph = (ph ^ ST_PH) | ST_ANY;
       sm.stat_m[t][row] = m;
