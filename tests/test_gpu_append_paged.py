@@ -31,7 +31,7 @@ def check(new, total, Hq, Hkv, block, dtype, seed=0, rot=128, inter=False, eps=1
     put = lambda t: None if t is None else t.cuda()  # noqa: E731
     got = fa.append_paged(xd[:, Hq:Hq + Hkv], xd[:, Hq + Hkv:], kd, vd, table.cuda(), lens.cuda(),
                           cu_tokens=None if no_cu else cu.cuda(), rope=put(rope), q=xd[:, :Hq] if with_q else None,
-                          q_weight=put(qw) if with_q else None, k_weight=put(kw), eps=eps, interleaved=inter, q_out=q_out)
+                          q_weight=put(qw), k_weight=put(kw), eps=eps, interleaved=inter, q_out=q_out)
     torch.cuda.synchronize()
     assert fa.device_status() == fa.FA_OK
     want_k, want_v, bound = kp.double(), vp.double(), torch.zeros(kp.shape, dtype=torch.float64)

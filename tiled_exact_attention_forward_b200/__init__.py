@@ -756,7 +756,7 @@ def append_paged(k, v, kpool, vpool, block_table, seqlens, cu_tokens=None, rope=
     array serves extend_paged and decode_paged.
     Keys are normed (eps given, weight k_weight or ones) and turned by rope as in
     norm_rope; values are copied.  q, packed [T, Hq, d], is normed with q_weight and
-    turned in the same launch: returned contiguous (None without q).
+    turned in the same launch: returned contiguous (None without q, q_weight then unused).
     A token without a place (position outside the cache or the table, block id outside
     the pool) is not written and reported by device_status().
     """
@@ -775,8 +775,8 @@ def append_paged(k, v, kpool, vpool, block_table, seqlens, cu_tokens=None, rope=
         q_out = _out_like(q, q_out)
         if not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous")
-    elif q_out is not None or q_weight is not None:
-        raise ValueError("q_out and q_weight need q")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
     _launch(_lib().fa_append_paged, "fa_append_paged", device, k.data_ptr(), v.data_ptr(), _addr(q), _addr(q_out),
             kpool.data_ptr(), vpool.data_ptr(), block_table.data_ptr(), _addr(cu_tokens), seqlens.data_ptr(), q_stride,
             k_stride, v_stride, _addr(q_weight), _addr(k_weight), _addr(rope), T, B, Hq, Hkv, num_blocks, bs, max_blocks,
