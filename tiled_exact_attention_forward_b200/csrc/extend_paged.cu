@@ -33,14 +33,16 @@
 //
 // What bounds it, and what it measured (device time):
 //   2048 tokens of a prompt at 14336 .. 16383, 32 heads over 8: the tensor cores through
-//     the S -> softmax -> PV chain of a two-tile item, as in fwd_tc.cu; 422 us, 1220 TFLOP/s;
-//   64 single tokens, 512 .. 8192 keys, 32 heads over 8: the cache's bytes; 199 us,
-//     5.7 TB/s (87 % of the copy rate): a CTA's share is some 120 key tiles of a few items,
-//     and an item's edges (Q, first S, last PV, epilogue) cost as much as one or two tiles;
-//   24 x 5 tokens, 100 .. 4000 keys, 16 heads over 16: 93 us, 5.1 TB/s (78 %), shorter items;
-//   17 ragged pieces under a window of 1024: 98 us, 500 TFLOP/s: half the key tiles are
-//     partly masked, and some 35 units a CTA leave little to level out between CTAs;
-//   one token over 512 keys: 14.1 us: launch, planning, four key tiles' latency, the join.
+//     the S -> softmax -> PV chain of a two-tile item, as in fwd_tc.cu; 425 us, 1210 TFLOP/s;
+//   64 single tokens, 512 .. 8192 keys, 32 heads over 8: the cache's bytes; 196 us, 5.8 TB/s
+//     (88 % of the copy rate); an item's edges (Q, first S, last PV, epilogue) cost as much
+//     as one or two key tiles, of the 118 a CTA takes here;
+//   24 x 5 tokens, 100 .. 4000 keys, 16 heads over 16: 90 us, 5.3 TB/s (80 %), shorter items;
+//   512 single tokens over 600 keys: 316 us, 4.0 TB/s (61 %): five key tiles an item, the
+//     edges' chains no longer hidden by the next item's loads (two stages a ring);
+//   17 ragged pieces under a window of 1024: 95 us, 515 TFLOP/s: a third of the key
+//     tiles are partly masked, and a CTA has 27 in three or four items to level out;
+//   one token over 512 keys: 14.2 us: launch, planning, a key tile's latency, the join.
 // The kernel's text is kept near 90 KB with single issue sites and loops that are not
 // unrolled: at 225 KB the sixteen warps' roles displaced one another in the instruction cache.
 #include <atomic>
@@ -1072,8 +1074,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         char* out = part ? reinterpret_cast<char*>(args.ws_o) : static_cast<char*>(args.o);
         at *= part ? D * 4 : D * 2;  // bytes from here on
         if (mine > 0) {
-          // Each lane writes its own row, 32 or 64 bytes a step.  (Rows put_aside in shared memory and
-          // written in runs of 128 bytes were no faster: 107 us for 108 on the ragged batch.)
+          // Each lane writes its own row, 32 or 64 bytes a step.  (Rows put aside in shared memory and
+          // written in runs were no faster: 107 us for 108 on the ragged batch; few rows joined there
+          // and written whole, so that both slots are free at once: 512 single tokens 316 -> 310 us,
+          // but 5 drafted tokens 90.2 -> 91.5 and one token 14.3 -> 14.8.)
           char* dst = out + at;
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
