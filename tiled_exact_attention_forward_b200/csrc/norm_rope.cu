@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const __grid_constan
 // block walks its tensor's tiles a grid's share apart and keeps its part of dw in
 // registers, so the weight gradients cost one partial row per block, which
 // sum_partials_kernel adds in a fixed order (no atomics: the result does not depend on
-// timing).
+// timing).  (The next tile's rows copied to shared memory meanwhile, with asynchronous
+// copies, measured 67.6 for 64.4 us.)
 template <class E, int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(THREADS)
     norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, unsigned tiles, unsigned blocks_q) {
