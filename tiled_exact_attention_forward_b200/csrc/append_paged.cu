@@ -10,10 +10,11 @@
 // Bound by memory for many tokens (each row read once and written once), by the
 // chain cu_tokens -> seqlens -> block_table -> store for few: the rows' loads are
 // issued ahead of that chain, and 16 lanes search cu_tokens together.  Measured: 16384
-// tokens of 32 heads in 16-row blocks 83.5 us, 6.4 TB/s (98 % of the copy rate); 64
-// single tokens with their queries 3.9 us, nearly all of it launch and that chain.
+// tokens of 32 heads in 16-row blocks 83.6 us, 6.5 TB/s (99 % of the copy rate); 64
+// single tokens with their queries 3.5 us (4.1 without the dependent launch), nearly all of it launch and that chain.
 #include "cache_ops.h"
 #include "common.cuh"
+#include "dependent.cuh"
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -57,6 +58,8 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
   const void* src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
   const long long stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
   const Lane l = lane_of<E, D, INTER>(s, a.rot);
+  wait_for_previous_kernel();
+  let_next_kernel_start();
 
   uint2 rlo[HG], rhi[HG];
   const char* x = static_cast<const char*>(src) + (t * stride + static_cast<long long>(h0) * D) * 2;
@@ -142,8 +145,7 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto kernel = a.interleaved ? (a.norm ? append_kernel<E, true, true> : append_kernel<E, true, false>)
                               : (a.norm ? append_kernel<E, false, true> : append_kernel<E, false, false>);
-  kernel<<<static_cast<unsigned>(blocks), THREADS, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(blocks)), dim3(THREADS), 0, stream, a);
 }
 
 }  // namespace app

@@ -79,6 +79,8 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const __grid_constan
   const bool live = p < static_cast<unsigned>(a.B) * static_cast<unsigned>(a.N);
   const Place at = place_of(a, live ? p : 0u);
   const Lane l = lane_of<E, D, INTER>(s, a.rot);
+  wait_for_previous_kernel();
+  let_next_kernel_start();
 
   const char* x = row_at<E>(a.x[t], a.x_stride[t], at, h0);
   const long long xh = a.x_stride[t][1] * elem_bytes<E>();
@@ -124,6 +126,7 @@ template <class E, int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(THREADS)
     norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, unsigned tiles, unsigned blocks_q) {
   constexpr int L = D / 8, P = positions_per_block<D>(), HG = heads_per_group<E>();
+  wait_for_previous_kernel();
   let_next_kernel_start();
   const int s = threadIdx.x % L;
   const Lane l = lane_of<E, D, INTER>(s, a.rot);
@@ -241,18 +244,17 @@ cudaError_t launch(const NormRopeArgs& a, bool backward, cudaStream_t stream) {
   const long long gq = (a.H[0] + HG - 1) / HG, gk = (a.H[1] + HG - 1) / HG;
   if (positions > 0x7fffffffLL || tiles * (gq + gk) > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (!backward) {
-    (a.norm ? norm_rope_kernel<E, D, INTER, true> : norm_rope_kernel<E, D, INTER, false>)
-        <<<static_cast<unsigned>(tiles * (gq + gk)), THREADS, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(a.norm ? norm_rope_kernel<E, D, INTER, true> : norm_rope_kernel<E, D, INTER, false>,
+                            dim3(static_cast<unsigned>(tiles * (gq + gk))), dim3(THREADS), 0, stream, a);
   }
   // Blocks in proportion to the tensors' tiles, at least one each.
   const long long all = tiles * (gq + gk) < kNormRopeBlocks ? tiles * (gq + gk) : kNormRopeBlocks;
   long long bk = gk == 0 ? 0 : (all * gk + gq + gk - 1) / (gq + gk);
   if (bk > all - 1) bk = all - 1;
   const unsigned blocks_q = static_cast<unsigned>(all - bk), blocks = static_cast<unsigned>(all);
-  (a.norm ? norm_rope_bwd_kernel<E, D, INTER, true> : norm_rope_bwd_kernel<E, D, INTER, false>)
-      <<<blocks, THREADS, 0, stream>>>(a, static_cast<unsigned>(tiles), blocks_q);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_dependent(a.norm ? norm_rope_bwd_kernel<E, D, INTER, true> : norm_rope_bwd_kernel<E, D, INTER, false>,
+                       dim3(blocks), dim3(THREADS), 0, stream, a, static_cast<unsigned>(tiles), blocks_q);
   if (e != cudaSuccess || !a.norm || a.partials == nullptr) return e;
   return launch_dependent(sum_partials_kernel<E>, dim3(D / 32, gk ? 2 : 1), dim3(1024), 0, stream, a,
                           static_cast<int>(blocks_q), static_cast<int>(blocks));
