@@ -30,9 +30,7 @@ The ring (context-parallel) forward over torch.distributed ranks sits in
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
-import struct
 
 import torch
 
@@ -471,77 +469,28 @@ def attention(q, k, v, causal: bool = False, window: int = 0, scale=None):
     return _Attention.apply(q, k, v, bool(causal), int(window), scale)
 
 
-# The calls below are made once or more per layer and token, so their host time counts:
-# checks are plain comparisons, pointers and strides go to the C ABI as integers and
-# packed bytes (about 25 microseconds a call became 12).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_pack12 = struct.Struct("12q").pack
-_pack18 = struct.Struct("18q").pack
+# The calls below are made once or more per layer and token, so their host time counts: their
+# checks, allocations and the C ABI's call are compiled (csrc/calls.cpp), and take their
+# arguments by position.
+_COMPILED = None
 
 
-def _on(first, *others):
-    """The CUDA device index of `first`; every other given tensor must sit there (None: skipped)."""
-    i = first.get_device()
-    if i < 0:
-        raise ValueError("tensors must be on a CUDA device (there is no CPU path)")
-    for t in others:
-        if t is not None and t.get_device() != i:
-            raise ValueError("tensors must all be on the same CUDA device")
-    return i
-
-
-def _launch(fn, name, device, *args):
-    """fn(*args, stream) with `device` current and its current stream; raises on a non-FA_OK status."""
-    if _current_device() == device:
-        st = fn(*args, _raw_stream(device))
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, _raw_stream(device))
-    if st != FA_OK:
-        raise FAError(st, name)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _need_int32(name, t, shape):
-    if t.shape != shape or t.dtype != torch.int32 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
-
-
-def _strides(t, packed):
-    """(batch, head, row) strides of a [B, H, N, d] or packed [T, H, d] tensor with contiguous rows."""
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError("the rows (last dimension) of q, k, their outputs and gradients must be contiguous")
-    return (0, st[1], st[0]) if packed else st[:3]
-
-
-def _qk_sizes(q, k):
-    """(B, Hq, Hk, N, d, packed) of queries and keys, [B, H, N, d] or packed [T, H, d]."""
-    shape = q.shape
-    packed = len(shape) == 3
-    if packed:
-        N, Hq, d = shape
-        B = 1
-    elif len(shape) == 4:
-        B, Hq, N, d = shape
-    else:
-        raise ValueError("q must be [B, H, N, d] or packed [T, H, d]")
-    if k is None:
-        return B, Hq, 0, N, d, packed
-    Hk = k.shape[1]
-    if k.shape != ((N, Hk, d) if packed else (B, Hk, N, d)) or k.dtype != q.dtype:
-        raise ValueError("q and k must share dtype and every size but the heads")
-    return B, Hq, Hk, N, d, packed
-
-
-def _grad_like(t):
-    """An uninitialised gradient laid out as t where t is dense, contiguous where not (expanded views)."""
-    g = torch.empty_like(t)
-    return g if g.stride(-1) == 1 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+def _compiled():
+    global _COMPILED
+    if _COMPILED is None:
+        lib = _lib()
+        try:
+            from . import _calls
+        except ImportError as e:
+            raise ImportError(
+                f"_calls.so is missing or was built for another Python or torch ({e}): build it with "
+                "`python -m tiled_exact_attention_forward_b200.build`"
+            ) from e
+        entries = (lib.fa_norm_rope, lib.fa_norm_rope_backward, lib.fa_norm_rope_backward_workspace_size,
+                   lib.fa_append_paged, lib.fa_extend_paged, lib.fa_extend_paged_workspace_size)
+        _calls.bind(FAError, *(ctypes.cast(f, ctypes.c_void_p).value for f in entries))
+        _COMPILED = _calls
+    return _COMPILED
 
 
 def _readable(g):
@@ -551,54 +500,6 @@ def _readable(g):
         if all(n < 2 or st * e % 16 == 0 for n, st in zip(g.shape[:-1], g.stride())):
             return g
     return g.clone(memory_format=torch.contiguous_format)
-
-
-def _rotation_args(dtype, q_weight, k_weight, rope, eps, d):
-    """(rot, max_pos, eps for the C ABI, weight dtype code) of a norm and rotation."""
-    rot = max_pos = 0
-    if rope is not None:
-        shape = rope.shape
-        if len(shape) != 2 or rope.dtype != torch.float32 or not rope.is_contiguous():
-            raise ValueError("rope must be a contiguous float32 tensor [positions, rot]: rot/2 cosines, rot/2 sines")
-        max_pos, rot = shape
-        if rot == 0 or rot % 16 or rot > d:
-            raise ValueError("rope's second dimension must be a multiple of 16 up to the head dimension")
-    if eps is None:
-        if q_weight is not None or k_weight is not None:
-            raise ValueError("weights need eps: without it there is no norm")
-        return rot, max_pos, -1.0, _dtype_code(dtype)
-    if not eps >= 0:
-        raise ValueError("eps must be >= 0 (None: no norm)")
-    wdt = None
-    for w in (q_weight, k_weight):
-        if w is not None:
-            t = w.dtype
-            if w.shape != (d,) or not w.is_contiguous():
-                raise ValueError("weights must be contiguous tensors of the head dimension")
-            if (t != dtype and t != torch.float32) or (wdt is not None and t != wdt):
-                raise ValueError("weights must share one dtype: the tensors' or float32")
-            wdt = t
-    return rot, max_pos, float(eps), _dtype_code(dtype if wdt is None else wdt)
-
-
-def _position_stride(positions, B, N):
-    if positions is None:
-        return 0
-    if positions.dtype != torch.int32 or positions.shape not in ((N,), (B, N)) or not positions.is_contiguous():
-        raise ValueError("positions must be a contiguous int32 tensor [N] or [B, N] (packed: [T])")
-    return N if positions.dim() == 2 else 0
-
-
-def _out_like(x, out):
-    """An output of x's sizes: the given one, checked, or a new contiguous one."""
-    if out is None:
-        return torch.empty_like(x, memory_format=torch.contiguous_format)
-    if out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("an output must have its input's shape and dtype")
-    return out
-
-
-_NO_STRIDES = (0, 0, 0)
 
 
 def norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6,
@@ -620,25 +521,9 @@ def norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=None
     calls take them; without k, q_out alone.  q_out, k_out may be given (at any
     strides, the inputs themselves among them).
     """
-    device = _on(q, k, q_weight, k_weight, rope, positions, q_out, k_out)
-    B, Hq, Hk, N, d, packed = _qk_sizes(q, k)
-    if k is None and (k_weight is not None or k_out is not None):
-        raise ValueError("k_weight and k_out need k")
-    rot, max_pos, e, wcode = _rotation_args(q.dtype, q_weight, k_weight, rope, eps, d)
-    pos_stride = _position_stride(positions, B, N)
-    q_out = _out_like(q, q_out)
-    ks = kos = _NO_STRIDES
-    if k is not None:
-        k_out = _out_like(k, k_out)
-        ks, kos = _strides(k, packed), _strides(k_out, packed)
-    strides = _pack12(*_strides(q, packed), *ks, *_strides(q_out, packed), *kos)
-    _launch(_lib().fa_norm_rope, "fa_norm_rope", device, q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out),
-            strides, _addr(q_weight), _addr(k_weight), _addr(rope), _addr(positions), pos_stride, B, Hq, Hk, N, d, rot, max_pos, e, int(bool(interleaved)),
-            _dtype_code(q.dtype), wcode)
-    return (q_out, k_out) if k is not None else q_out
+    return (_COMPILED or _compiled()).norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved, q_out, k_out)
 
 
-@functools.lru_cache(maxsize=None)
 def norm_rope_backward_workspace_size(d) -> int:
     return int(_lib().fa_norm_rope_backward_workspace_size(d))
 
@@ -653,36 +538,8 @@ def norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope=
     A weight that is None has no gradient (None); weight gradients are summed in
     float32 in a fixed order and come in the weights' dtype.
     """
-    device = _on(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, workspace)
-    if (k is None) != (dk_out is None):
-        raise ValueError("k and dk_out go together")
-    B, Hq, Hk, N, d, packed = _qk_sizes(q, k)
-    if dq_out.shape != q.shape or dq_out.dtype != q.dtype:
-        raise ValueError("dq_out must have q's shape and dtype")
-    dq, dk = _grad_like(q), None
-    ks = kgs = dks = _NO_STRIDES
-    if k is not None:
-        if dk_out.shape != k.shape or dk_out.dtype != k.dtype:
-            raise ValueError("dk_out must have k's shape and dtype")
-        dk = _grad_like(k)
-        ks, kgs, dks = _strides(k, packed), _strides(dk_out, packed), _strides(dk, packed)
-    elif k_weight is not None:
-        raise ValueError("k_weight needs k")
-    rot, max_pos, e, wcode = _rotation_args(q.dtype, q_weight, k_weight, rope, eps, d)
-    pos_stride = _position_stride(positions, B, N)
-    dqw = None if q_weight is None else torch.empty_like(q_weight)
-    dkw = None if k_weight is None else torch.empty_like(k_weight)
-    strides = _pack18(*_strides(q, packed), *ks, *_strides(dq_out, packed), *kgs, *_strides(dq, packed), *dks)
-    ws_bytes = 0
-    if dqw is not None or dkw is not None:
-        if workspace is None:
-            workspace = q.new_empty((norm_rope_backward_workspace_size(d),), dtype=torch.uint8)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _launch(_lib().fa_norm_rope_backward, "fa_norm_rope_backward", device, q.data_ptr(), _addr(k), dq_out.data_ptr(),
-            _addr(dk_out), dq.data_ptr(), _addr(dk), strides, _addr(q_weight), _addr(k_weight), _addr(dqw), _addr(dkw),
-            _addr(rope), _addr(positions), pos_stride, B, Hq, Hk,
-            N, d, rot, max_pos, e, int(bool(interleaved)), _dtype_code(q.dtype), wcode, _addr(workspace), ws_bytes)
-    return dq, dk, dqw, dkw
+    return (_COMPILED or _compiled()).norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, eps,
+                                                         interleaved, workspace)
 
 
 class _QKNormRope(torch.autograd.Function):
@@ -715,35 +572,6 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=N
     return _QKNormRope.apply(q, k, q_weight, k_weight, rope, positions, eps, bool(interleaved))
 
 
-def _token_stride(name, t, T, H, d, dtype):
-    """The token stride of a packed [T, H, d] tensor whose heads are contiguous."""
-    if t.shape != (T, H, d) or t.dtype != dtype:
-        raise ValueError(f"{name} must be packed [{T}, {H}, {d}] with the pools' dtype")
-    st = t.stride()
-    if st[2] != 1 or (st[1] != d and H > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return st[0]
-
-
-def _paged_sizes(kpool, vpool, block_table, seqlens, cu_tokens, T):
-    """(num_blocks, Hkv, block_size, d, B, max_blocks) of a paged cache, its tensors checked."""
-    shape = kpool.shape
-    if len(shape) != 4 or vpool.shape != shape or vpool.dtype != kpool.dtype:
-        raise ValueError("kpool and vpool must be [num_blocks, Hkv, block_size, d] and share dtype")
-    if not (kpool.is_contiguous() and vpool.is_contiguous()):
-        raise ValueError("kpool and vpool must be contiguous")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be an int32 tensor of shape [B, max_blocks]")
-    B, max_blocks = block_table.shape
-    _need_int32("block_table", block_table, (B, max_blocks))
-    _need_int32("seqlens", seqlens, (B,))
-    if cu_tokens is not None:
-        _need_int32("cu_tokens", cu_tokens, (B + 1,))
-    elif T != B:
-        raise ValueError("without cu_tokens there is one token for each sequence")
-    return (*shape, B, max_blocks)
-
-
 def append_paged(k, v, kpool, vpool, block_table, seqlens, cu_tokens=None, rope=None, q=None, q_weight=None,
                  k_weight=None, eps=None, interleaved: bool = False, q_out=None):
     """New tokens' keys and values into a paged cache, in place, the keys rotated on the way.
@@ -760,31 +588,10 @@ def append_paged(k, v, kpool, vpool, block_table, seqlens, cu_tokens=None, rope=
     A token without a place (position outside the cache or the table, block id outside
     the pool) is not written and reported by device_status().
     """
-    device = _on(k, v, kpool, vpool, block_table, seqlens, cu_tokens, rope, q, q_weight, k_weight, q_out)
-    T = k.shape[0]
-    dtype = kpool.dtype
-    num_blocks, Hkv, bs, d, B, max_blocks = _paged_sizes(kpool, vpool, block_table, seqlens, cu_tokens, T)
-    k_stride, v_stride = _token_stride("k", k, T, Hkv, d, dtype), _token_stride("v", v, T, Hkv, d, dtype)
-    rot, max_pos, e, wcode = _rotation_args(dtype, q_weight, k_weight, rope, eps, d)
-    Hq = q_stride = 0
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be packed [T, Hq, d]")
-        Hq = q.shape[1]
-        q_stride = _token_stride("q", q, T, Hq, d, dtype)
-        q_out = _out_like(q, q_out)
-        if not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous")
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    _launch(_lib().fa_append_paged, "fa_append_paged", device, k.data_ptr(), v.data_ptr(), _addr(q), _addr(q_out),
-            kpool.data_ptr(), vpool.data_ptr(), block_table.data_ptr(), _addr(cu_tokens), seqlens.data_ptr(), q_stride,
-            k_stride, v_stride, _addr(q_weight), _addr(k_weight), _addr(rope), T, B, Hq, Hkv, num_blocks, bs, max_blocks,
-            d, rot, max_pos, e, int(bool(interleaved)), _dtype_code(dtype), wcode)
-    return q_out
+    return (_COMPILED or _compiled()).append_paged(k, v, kpool, vpool, block_table, seqlens, cu_tokens, rope, q, q_weight,
+                                                   k_weight, eps, interleaved, q_out)
 
 
-@functools.lru_cache(maxsize=4096)
 def extend_paged_workspace_size(T, Hq, Hkv, d) -> int:
     return int(_lib().fa_extend_paged_workspace_size(T, Hq, Hkv, d))
 
@@ -803,29 +610,8 @@ def extend_paged(q, kpool, vpool, block_table, seqlens, cu_tokens=None, causal: 
     may overlap need workspaces of their own (the default makes one).  An out-of-range
     block id of a used block is skipped and reported by device_status().
     """
-    device = _on(q, kpool, vpool, block_table, seqlens, cu_tokens, workspace, out, lse)
-    if q.dim() != 3:
-        raise ValueError("q must be packed [T, Hq, d]")
-    T, Hq = q.shape[:2]
-    dtype = kpool.dtype
-    num_blocks, Hkv, bs, d, B, max_blocks = _paged_sizes(kpool, vpool, block_table, seqlens, cu_tokens, T)
-    q_stride = _token_stride("q", q, T, Hq, d, dtype)
-    if Hkv < 1 or Hq % Hkv:
-        raise ValueError("the query heads must be a multiple of the pools' heads")
-    out = _out_like(q, out)
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
-    if lse is None:
-        lse = q.new_empty((T, Hq), dtype=torch.float32)
-    elif lse.shape != (T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 tensor [T, Hq]")
-    if workspace is None:
-        workspace = q.new_empty(max(extend_paged_workspace_size(T, Hq, Hkv, d), 256), dtype=torch.uint8)
-    _launch(_lib().fa_extend_paged, "fa_extend_paged", device, q.data_ptr(), kpool.data_ptr(), vpool.data_ptr(),
-            block_table.data_ptr(), _addr(cu_tokens), seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), q_stride, T, B,
-            Hq, Hkv, num_blocks, bs, max_blocks, d, _scale_arg(scale), int(bool(causal)), int(window),
-            _dtype_code(dtype), workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    return out, lse
+    return (_COMPILED or _compiled()).extend_paged(q, kpool, vpool, block_table, seqlens, cu_tokens, causal, window,
+                                                   _scale_arg(scale), workspace, out, lse)
 
 
 def selftest_wait_timeout(limit_cycles: int = 20_000_000, device=None) -> int:

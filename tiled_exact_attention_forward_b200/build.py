@@ -14,6 +14,9 @@ norm-and-rotate kernels (float32 in and out among their types) are built without
 ``--use_fast_math`` so their exp2, log, square root and division are the
 IEEE-rounded ones; every other kernel calls its fast instructions explicitly and keeps the
 fast-math flags it was measured with.
+
+csrc/calls.cpp, the compiled side of some of the Python calls, becomes the extension
+module _calls.so beside it (host code only, against torch's headers).
 """
 from __future__ import annotations
 
@@ -23,6 +26,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -30,6 +34,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libfa_b200.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+CALLS_SOURCE = os.path.join(CSRC, "calls.cpp")
+CALLS_PATH = os.path.join(HERE, "_calls.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON_FLAGS = [
@@ -61,16 +67,16 @@ def flags_for(src: str):
 
 
 def _inputs():
-    files = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    files = [CALLS_SOURCE] + sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     files += glob.glob(os.path.join(ROOT, "include", "*.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(CALLS_PATH)):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -83,13 +89,35 @@ def _compile(src: str, extra, verbose: bool):
     return obj, r
 
 
+def calls_command(out: str):
+    """The host compiler's command for the extension module: the one torch was built to go with (a
+    compiler that links a C++ runtime of its own would not share its exceptions)."""
+    from torch.utils import cpp_extension
+
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    libs = ["torch_python", "torch", "torch_cpu", "torch_cuda", "c10", "c10_cuda"]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            *(f"-I{d}" for d in inc), "-o", out, CALLS_SOURCE,
+            *(f"-L{d}" for d in cpp_extension.library_paths()), *(f"-l{n}" for n in libs)]
+
+
+def _build_calls(verbose: bool):
+    tmp = CALLS_PATH + ".tmp"
+    cmd = calls_command(tmp)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return tmp, subprocess.run(cmd, cwd=CSRC, capture_output=True, text=True)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     """Compile every kernel for sm_100a into libfa_b200.so; returns its path."""
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 1)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 1)) as ex:
+        calls = ex.submit(_build_calls, verbose)
         results = list(ex.map(lambda s: _compile(s, extra_flags, verbose), srcs))
     objs = []
     for (obj, r), src in zip(results, srcs):
@@ -107,7 +135,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError(f"nvcc link failed with exit code {r.returncode}")
+    calls_tmp, r = calls.result()
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"the host compiler failed on calls.cpp with exit code {r.returncode}")
     os.replace(tmp, LIB_PATH)
+    os.replace(calls_tmp, CALLS_PATH)
     return LIB_PATH
 
 
