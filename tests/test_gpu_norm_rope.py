@@ -263,6 +263,22 @@ def test_gradients_as_autograd_lays_them_out(how):
     assert torch.equal(leaf.grad, want[0]) and torch.equal(lw.grad, want[2])
 
 
+def test_statuses_become_errors():
+    """What the C ABI refuses raises FAError and leaves the next call unharmed."""
+    x = torch.randn(1, 2, 4, 96, device="cuda")
+    with pytest.raises(fa.FAError) as e:
+        fa.norm_rope(x)
+    assert e.value.status == fa.FA_ERR_UNSUPPORTED
+    y = torch.randn(1, 2, 4, 66, device="cuda")[..., :64]  # rows 66 elements apart: not a multiple of 16 bytes
+    with pytest.raises(fa.FAError) as e:
+        fa.norm_rope(y)
+    assert e.value.status == fa.FA_ERR_INVALID
+    with pytest.raises(fa.FAError):
+        fa.norm_rope(torch.empty(1, 2, 0, 64, device="cuda"))
+    x = torch.ones(1, 2, 4, 64, device="cuda")
+    assert torch.allclose(fa.norm_rope(x, eps=0.0), x, atol=1e-6)
+
+
 def test_second_derivatives_are_refused():
     x = torch.randn(1, 1, 4, 64, device="cuda").requires_grad_()
     y = fa.qk_norm_rope(x, rope=rope_table(4, 64).cuda())

@@ -139,6 +139,15 @@ def test_binding_refuses_cpu_tensors():
             call()
 
 
+def test_binding_refuses_what_is_no_tensor_or_number():
+    q = torch.empty(1, 2, 8, 128, dtype=BF, device="meta")
+    for call in (lambda: fa.norm_rope("q"), lambda: fa.norm_rope(None), lambda: fa.norm_rope(q, k=3),
+                 lambda: fa.norm_rope(q, eps="1"), lambda: fa.norm_rope(q.double()),
+                 lambda: fa.extend_paged(q[0], q, q, q, None), lambda: fa.append_paged(1, 2, 3, 4, 5, 6)):
+        with pytest.raises(TypeError):
+            call()
+
+
 NOT_THE_DEVICE = r"^(?!.*CUDA)"
 
 
@@ -204,3 +213,14 @@ class TestBindingChecks:
         q = t(7, 128, 8).transpose(1, 2)
         with pytest.raises(ValueError, match="heads"):
             fa.extend_paged(q, t(5, 2, 16, 128), t(5, 2, 16, 128), t(3, 4, dtype=i32), t(3, dtype=i32), t(4, dtype=i32))
+
+    def test_window(self):
+        t, i32 = self.t, torch.int32
+        args = (t(7, 8, 128), t(5, 2, 16, 128), t(5, 2, 16, 128), t(3, 4, dtype=i32), t(3, dtype=i32), t(4, dtype=i32))
+        for window in (-1, 2 ** 31, -2 ** 62):
+            with pytest.raises(ValueError, match="window"):
+                fa.extend_paged(*args, window=window)
+        with pytest.raises((TypeError, OverflowError)):
+            fa.extend_paged(*args, window=2 ** 70)
+        with pytest.raises(ValueError, match="CUDA"):
+            fa.extend_paged(*args, window=5)
