@@ -1,6 +1,9 @@
 """Refusals of the norm-and-rotate, append and chunk attention calls: the C ABI returns before
 anything is launched, the binding raises before the C ABI is called (no GPU needed)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -137,6 +140,15 @@ def test_binding_refuses_cpu_tensors():
                  lambda: fa.extend_paged(torch.zeros(1, 2, 128, dtype=BF), pool, pool, table, lens)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_unbound_module_refuses_calls():
+    code = ("import torch; from tiled_exact_attention_forward_b200 import _calls\n"
+            "try: _calls.norm_rope(*[None] * 10)\n"
+            "except RuntimeError as e: assert 'not bound' in str(e)\n"
+            "else: raise SystemExit(1)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(fa.__file__)))
+    assert subprocess.run([sys.executable, "-c", code], cwd=root).returncode == 0
 
 
 def test_binding_refuses_what_is_no_tensor_or_number():

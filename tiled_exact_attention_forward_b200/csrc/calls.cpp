@@ -392,18 +392,6 @@ PyObject* extend_paged(PyObject* const* a, Py_ssize_t n) {
 }
 
 // ---------------------------------------------------------------- the module
-// Exceptions become Python's: the checks' ValueError and TypeError, the allocator's out-of-memory error.
-template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
-PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  HANDLE_TH_ERRORS
-  try {
-    return F(a, n);
-  } catch (const Failed&) {
-    return nullptr;
-  }
-  END_HANDLE_TH_ERRORS
-}
-
 // bind(exception class, the six entry points' addresses in the order of `abi`)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   arguments(n, 7);
@@ -424,6 +412,19 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   Py_INCREF(a[0]);
   fa_error = a[0];
   Py_RETURN_NONE;
+}
+
+// Exceptions become Python's: the checks' ValueError and TypeError, the allocator's out-of-memory error.
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  try {
+    TORCH_CHECK(F == bind || fa_error != nullptr, "the library is not bound: call through the package");
+    return F(a, n);
+  } catch (const Failed&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
 }
 
 #define FA_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<name>)), METH_FASTCALL, nullptr}
