@@ -1294,6 +1294,7 @@ constexpr int CB_WARPS = 8, CB_ROWS = 4;
 template <class T>
 __global__ void __launch_bounds__(CB_WARPS * 32) combine_kernel(const __grid_constant__ ExtendArgs args) {
   wait_for_previous_kernel();
+  let_next_kernel_start();
   const ExtendDesc d = args.desc[blockIdx.x];
   if (d.last < 0) return;
   const int lane = threadIdx.x & 31;
