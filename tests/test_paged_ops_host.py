@@ -236,3 +236,17 @@ class TestBindingChecks:
             fa.extend_paged(*args, window=2 ** 70)
         with pytest.raises(ValueError, match="CUDA"):
             fa.extend_paged(*args, window=5)
+
+    def test_workspace_of_fewer_bytes_than_elements(self):
+        """An expanded or strided workspace would be written past its memory."""
+        t, i32 = self.t, torch.int32
+        q = t(1, 2, 8, 128)
+        args = (t(7, 8, 128), t(5, 2, 16, 128), t(5, 2, 16, 128), t(3, 4, dtype=i32), t(3, dtype=i32), t(4, dtype=i32))
+        u8 = torch.uint8
+        for ws in (t(1, dtype=u8).expand(1 << 26), t(1 << 20, 128, dtype=u8)[:, :64], t(1 << 27, dtype=u8)[::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                fa.norm_rope_backward(q, None, q, None, t(128), workspace=ws)
+            with pytest.raises(ValueError, match="workspace"):
+                fa.extend_paged(*args, workspace=ws)
+        with pytest.raises(ValueError, match="CUDA"):
+            fa.extend_paged(*args, workspace=t(1 << 26, dtype=u8))

@@ -108,6 +108,10 @@ void check_out(const Tensor& x, const Opt& out) {
   TORCH_CHECK_VALUE(!out || (out->sizes() == x.sizes() && out->scalar_type() == x.scalar_type()),
                     "an output must have its input's shape and dtype");
 }
+// A workspace's bytes are written as one run: an expanded or strided one has fewer than its elements'.
+void check_workspace(const Opt& ws) {
+  TORCH_CHECK_VALUE(!ws || ws->is_contiguous(), "workspace must be contiguous");
+}
 Tensor bytes(const Tensor& like, size_t n) {
   return at::empty({static_cast<int64_t>(n)}, at::TensorOptions(like.device()).dtype(at::kByte));
 }
@@ -245,6 +249,7 @@ PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(gq.sizes() == q.sizes() && gq.scalar_type() == q.scalar_type(), "dq_out must have q's shape and dtype");
   TORCH_CHECK_VALUE(!k || (gk->sizes() == k->sizes() && gk->scalar_type() == k->scalar_type()),
                     "dk_out must have k's shape and dtype");
+  check_workspace(ws);
   const Turn t = turn_of(q.scalar_type(), qw, kw, rope, a[8], r.d);
   const long long ps = position_stride(pos, r);
   const int inter = truth(a[9]);
@@ -367,6 +372,7 @@ PyObject* extend_paged(PyObject* const* a, Py_ssize_t n) {
                            l->is_contiguous()),
                     "lse must be a contiguous float32 tensor [T, Hq]");
   TORCH_CHECK_VALUE(!o || o->is_contiguous(), "out must be contiguous");
+  check_workspace(ws);
   const int causal = truth(a[6]);
   const long long window = PyLong_AsLongLong(a[7]);
   if (window == -1 && PyErr_Occurred()) throw Failed{};
