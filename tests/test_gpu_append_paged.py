@@ -114,6 +114,51 @@ def test_tokens_without_a_place_are_left_out():
         assert torch.equal(vd.cpu().nan_to_num(9.0), want_v.nan_to_num(9.0))
 
 
+@pytest.mark.parametrize("rot,eps", [(128, 1e-6), (64, None), (0, 1e-6)])
+def test_a_token_without_a_place_has_no_query_either(rot, eps):
+    """A block id outside the pool, a position below 0 and one past the cache: the token's key and value
+    are not written and its query is NaN where it would be turned; all else is as without them."""
+    new, total, Hq, Hkv, block = [4, 4, 4, 3], [20, 20, 20, 9], 6, 2, 8
+    x, kp, vp, table, cu, lens, qw, kw, rope = make(new, total, Hq, Hkv, block, FP16, seed=6, rot=rot)
+    rope = rope_table(32, rot) if rot else None
+    if eps is None:
+        qw = kw = None
+    put = lambda t: None if t is None else t.cuda()  # noqa: E731
+
+    def run(table, lens):
+        kd, vd, xd = kp.cuda(), vp.cuda(), x.cuda()
+        q = fa.append_paged(xd[:, Hq:Hq + Hkv], xd[:, Hq + Hkv:], kd, vd, table.cuda(), lens.cuda(), cu_tokens=cu.cuda(),
+                            rope=put(rope), q=xd[:, :Hq], q_weight=put(qw), k_weight=put(kw), eps=eps)
+        return fa.device_status(), q.cpu(), kd.cpu(), vd.cpu()
+
+    status, q, kd, vd = run(table, lens)
+    assert status == fa.FA_OK
+    for bad_id in (-1, kp.shape[0], 2 ** 31 - 1):
+        t2, l2 = table.clone(), lens.clone()
+        t2[0, 2] = bad_id                # sequence 0's tokens, positions 16 .. 19
+        l2[1] = 2                        # sequence 1: positions -2 .. 1, two below 0
+        l2[2] = 26                       # sequence 2: positions 22 .. 25, two past the 24 that the table holds
+        status, q2, kd2, vd2 = run(t2, l2)
+        assert status == fa.FA_ERR_INVALID
+        lost = [0, 1, 2, 3, 4, 5, 10, 11]
+        moved = [6, 7, 8, 9]             # written at other positions than before
+        same = [12, 13, 14]
+        assert torch.equal(q2[same], q[same]) and q2[moved].isfinite().all()
+        if rot:
+            assert q2[lost][..., :rot].isnan().all()
+        if rot < 128:
+            assert torch.equal(q2[lost][..., rot:], q[lost][..., rot:])
+        want_k, want_v = kp.clone(), vp.clone()
+        for t, b, pos in ((6, 1, 0), (7, 1, 1), (8, 2, 22), (9, 2, 23), (12, 3, 6), (13, 3, 7), (14, 3, 8)):
+            at = (int(table[b, pos // block]), slice(None), pos % block)
+            r = None if rope is None else rope[pos]
+            z, bound = norm_rotate(x[t, Hq:Hq + Hkv], kw, r, eps, False)
+            assert_within(kd2[at], z, bound, f"key of token {t}")
+            want_k[at], want_v[at] = kd2[at], x[t, Hq + Hkv:]
+        assert torch.equal(kd2.nan_to_num(9.0), want_k.nan_to_num(9.0))
+        assert torch.equal(vd2.nan_to_num(9.0), want_v.nan_to_num(9.0))
+
+
 def test_pool_offsets_past_32_bits():
     """A pool of more than 2^31 elements: the last block is written at its place."""
     block, Hkv = 4096, 8

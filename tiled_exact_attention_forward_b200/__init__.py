@@ -586,7 +586,8 @@ def append_paged(k, v, kpool, vpool, block_table, seqlens, cu_tokens=None, rope=
     norm_rope; values are copied.  q, packed [T, Hq, d], is normed with q_weight and
     turned in the same launch: returned contiguous (None without q, q_weight then unused).
     A token without a place (position outside the cache or the table, block id outside
-    the pool) is not written and reported by device_status().
+    the pool) is not written (its query comes out NaN where it would be turned) and
+    reported by device_status().
     """
     return (_COMPILED or _compiled()).append_paged(k, v, kpool, vpool, block_table, seqlens, cu_tokens, rope, q, q_weight,
                                                    k_weight, eps, interleaved, q_out)

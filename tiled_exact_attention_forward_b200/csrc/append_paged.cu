@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
   const long long cap = static_cast<long long>(a.max_blocks) << a.block_shift;
   bool good = placed && pos >= 0 && pos < cap && (a.rot == 0 || pos < a.max_pos);
   int phys = -1;
-  if (good && kind != 0) {
+  if (good) {  // for queries too: a token has all of its rows or none
     phys = a.block_table[static_cast<long long>(b) * a.max_blocks + (pos >> a.block_shift)];
     good = phys >= 0 && phys < a.num_blocks;
   }
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
                                          (pos & ((1 << a.block_shift) - 1));
   const long long next = (kind == 0 ? 1LL : 1LL << a.block_shift) * (D * 2);
   char* y = static_cast<char*>(dst) + row0 * (D * 2);
-  // A query without a place in the cache or the table comes out NaN where it is rotated.
+  // The query of a token without a place comes out NaN where it is rotated.
   const bool write = kind == 0 ? placed : good;
   Turn turn;
   if (kind < 2) {
