@@ -101,6 +101,12 @@ void check(fa_status st, const char* name) {
   throw Failed{};
 }
 
+// Raises the version of a tensor of the caller's that the call has written, as torch's in-place
+// operations do: autograd then refuses a backward pass that saved the values from before.
+void written(const Opt& t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 Tensor new_like(const Tensor& t) { return at::empty(t.sizes(), t.options().requires_grad(false)); }
 // The output for x: the given one, or a new contiguous one.
 Tensor out_like(const Tensor& x, const Opt& out) { return out ? *out : new_like(x); }
@@ -233,6 +239,8 @@ PyObject* norm_rope(PyObject* const* a, Py_ssize_t n) {
                       static_cast<const float*>(ptr(rope)), static_cast<const int32_t*>(ptr(pos)), ps, r.B, r.Hq, r.Hk, r.N,
                       r.d, t.rot, t.max_pos, t.eps, inter, code, t.weight, on.stream()),
         "fa_norm_rope");
+  written(qo);
+  written(ko);
   return k ? tuple({q_out, k_out}) : wrap(q_out);
 }
 
@@ -352,6 +360,9 @@ PyObject* append_paged(PyObject* const* a, Py_ssize_t n) {
                          static_cast<const float*>(ptr(rope)), T, p.B, Hq, p.Hkv, p.num_blocks, p.block_size, p.max_blocks,
                          p.d, t.rot, t.max_pos, t.eps, inter, code, t.weight, on.stream()),
         "fa_append_paged");
+  written(kp);
+  written(vp);
+  written(qo);
   return wrap(q_out);
 }
 
@@ -394,6 +405,8 @@ PyObject* extend_paged(PyObject* const* a, Py_ssize_t n) {
                          p.max_blocks, p.d, scale, causal, static_cast<int>(window), code, ws->data_ptr(), ws->nbytes(),
                          on.stream()),
         "fa_extend_paged");
+  written(o);
+  written(l);
   return tuple({out, lse});
 }
 
