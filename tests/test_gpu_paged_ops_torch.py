@@ -1,5 +1,8 @@
-"""The norm-and-rotate, append and chunk attention calls among torch's other operations: versions of
-tensors written in place."""
+"""The norm-and-rotate, append and chunk attention calls among torch's other operations and Python's
+other threads: versions of tensors written in place, calls that wait for the device."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -56,3 +59,38 @@ def test_inference_tensors_have_no_version():
         assert torch.equal(fa.extend_paged(q, kp, vp, table, lens, cu, out=torch.empty_like(q))[0],
                            fa.extend_paged(q, kp, vp, table, lens, cu)[0])
     assert fa.device_status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("which", ["norm_rope", "norm_rope_backward", "append_paged", "extend_paged"])
+def test_other_threads_run_while_a_launch_waits(which):
+    """The device is busy for about a second and its queue of launches fills up: a call then waits in the
+    driver, and another thread goes on meanwhile (it sleeps a millisecond a turn)."""
+    q, k, v, kp, vp, table, lens, cu = small_cache()
+    g, w = torch.ones_like(q), torch.ones(128, dtype=BF16, device="cuda")
+    call = {"norm_rope": lambda: fa.norm_rope(q),
+            "norm_rope_backward": lambda: fa.norm_rope_backward(q, None, g, None, w),
+            "append_paged": lambda: fa.append_paged(k, v, kp, vp, table, lens, cu),
+            "extend_paged": lambda: fa.extend_paged(q, kp, vp, table, lens, cu)}[which]
+    call()
+    torch.cuda.synchronize()
+    turns, done = [], threading.Event()
+
+    def tick():
+        while not done.is_set():
+            time.sleep(0.001)
+            turns.append(time.perf_counter())
+
+    t = threading.Thread(target=tick)
+    t.start()
+    torch.cuda._sleep(2_000_000_000)
+    begin = time.perf_counter()
+    for _ in range(1500):
+        call()
+    took = time.perf_counter() - begin
+    torch.cuda.synchronize()
+    done.set()
+    t.join()
+    assert took > 0.4, "the queue did not fill up"
+    during = [x for x in turns if begin <= x <= begin + took]
+    assert len(during) > 100
+    assert max(b - a for a, b in zip(during, during[1:])) < 0.25

@@ -107,6 +107,17 @@ void written(const Opt& t) {
   if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
 
+// Lets Python's other threads run for as long as it lives: a launch waits while the device's queue
+// is full, an allocation may wait for the device.  No Python object is touched meanwhile.
+struct OtherThreadsRun {
+  PyThreadState* state = PyEval_SaveThread();
+  ~OtherThreadsRun() { PyEval_RestoreThread(state); }
+};
+template <class F> auto without_gil(F f) {
+  const OtherThreadsRun others;
+  return f();
+}
+
 Tensor new_like(const Tensor& t) { return at::empty(t.sizes(), t.options().requires_grad(false)); }
 // The output for x: the given one, or a new contiguous one.
 Tensor out_like(const Tensor& x, const Opt& out) { return out ? *out : new_like(x); }
@@ -230,14 +241,18 @@ PyObject* norm_rope(PyObject* const* a, Py_ssize_t n) {
   if (k) check_out(*k, ko);
   On on(q);
   on.with(k).with(qw).with(kw).with(rope).with(pos).with(qo).with(ko);
-  const Tensor q_out = out_like(q, qo);
-  Opt k_out;
-  if (k) k_out = out_like(*k, ko);
-  strides_of(q_out, r.packed, st + 6);
-  if (k) strides_of(*k_out, r.packed, st + 9);
-  check(abi.norm_rope(q.data_ptr(), ptr(k), q_out.data_ptr(), ptr(k_out), st, ptr(qw), ptr(kw),
-                      static_cast<const float*>(ptr(rope)), static_cast<const int32_t*>(ptr(pos)), ps, r.B, r.Hq, r.Hk, r.N,
-                      r.d, t.rot, t.max_pos, t.eps, inter, code, t.weight, on.stream()),
+  Opt q_out, k_out;
+  check(without_gil([&] {
+          q_out = out_like(q, qo);
+          strides_of(*q_out, r.packed, st + 6);
+          if (k) {
+            k_out = out_like(*k, ko);
+            strides_of(*k_out, r.packed, st + 9);
+          }
+          return abi.norm_rope(q.data_ptr(), ptr(k), ptr(q_out), ptr(k_out), st, ptr(qw), ptr(kw),
+                               static_cast<const float*>(ptr(rope)), static_cast<const int32_t*>(ptr(pos)), ps, r.B, r.Hq,
+                               r.Hk, r.N, r.d, t.rot, t.max_pos, t.eps, inter, code, t.weight, on.stream());
+        }),
         "fa_norm_rope");
   written(qo);
   written(ko);
@@ -276,22 +291,26 @@ PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
     Tensor g = at::empty_like(x, x.options().requires_grad(false));
     return g.stride(-1) == 1 ? g : new_like(x);
   };
-  const Tensor dq = grad_like(q);
-  Opt dk, dqw, dkw;
-  if (k) dk = grad_like(*k);
-  if (qw) dqw = new_like(*qw);
-  if (kw) dkw = new_like(*kw);
-  strides_of(dq, r.packed, st + 12);
-  if (k) strides_of(*dk, r.packed, st + 15);
-  size_t ws_bytes = 0;
-  if (qw || kw) {
-    if (!ws) ws = bytes(q, abi.norm_rope_backward_workspace_size(r.d));
-    ws_bytes = ws->nbytes();
-  }
-  check(abi.norm_rope_backward(q.data_ptr(), ptr(k), gq.data_ptr(), ptr(gk), dq.data_ptr(), ptr(dk), st, ptr(qw), ptr(kw),
-                               ptr(dqw), ptr(dkw), static_cast<const float*>(ptr(rope)),
-                               static_cast<const int32_t*>(ptr(pos)), ps, r.B, r.Hq, r.Hk, r.N, r.d, t.rot, t.max_pos, t.eps,
-                               inter, code, t.weight, ptr(ws), ws_bytes, on.stream()),
+  Opt dq, dk, dqw, dkw;
+  check(without_gil([&] {
+          dq = grad_like(q);
+          strides_of(*dq, r.packed, st + 12);
+          if (k) {
+            dk = grad_like(*k);
+            strides_of(*dk, r.packed, st + 15);
+          }
+          if (qw) dqw = new_like(*qw);
+          if (kw) dkw = new_like(*kw);
+          size_t ws_bytes = 0;
+          if (qw || kw) {
+            if (!ws) ws = bytes(q, abi.norm_rope_backward_workspace_size(r.d));
+            ws_bytes = ws->nbytes();
+          }
+          return abi.norm_rope_backward(q.data_ptr(), ptr(k), gq.data_ptr(), ptr(gk), ptr(dq), ptr(dk), st, ptr(qw), ptr(kw),
+                                        ptr(dqw), ptr(dkw), static_cast<const float*>(ptr(rope)),
+                                        static_cast<const int32_t*>(ptr(pos)), ps, r.B, r.Hq, r.Hk, r.N, r.d, t.rot,
+                                        t.max_pos, t.eps, inter, code, t.weight, ptr(ws), ws_bytes, on.stream());
+        }),
         "fa_norm_rope_backward");
   return tuple({dq, dk, dqw, dkw});
 }
@@ -353,12 +372,14 @@ PyObject* append_paged(PyObject* const* a, Py_ssize_t n) {
   On on(k);
   on.with(v).with(kp).with(vp).with(table).with(lens).with(cu).with(rope).with(q).with(qw).with(kw).with(qo);
   Opt q_out;
-  if (q) q_out = out_like(*q, qo);
-  check(abi.append_paged(k.data_ptr(), v.data_ptr(), ptr(q), ptr(q_out), kp.data_ptr(), vp.data_ptr(),
-                         static_cast<const int32_t*>(table.data_ptr()), static_cast<const int32_t*>(ptr(cu)),
-                         static_cast<const int32_t*>(lens.data_ptr()), qs, ks, vs, ptr(qw), ptr(kw),
-                         static_cast<const float*>(ptr(rope)), T, p.B, Hq, p.Hkv, p.num_blocks, p.block_size, p.max_blocks,
-                         p.d, t.rot, t.max_pos, t.eps, inter, code, t.weight, on.stream()),
+  check(without_gil([&] {
+          if (q) q_out = out_like(*q, qo);
+          return abi.append_paged(k.data_ptr(), v.data_ptr(), ptr(q), ptr(q_out), kp.data_ptr(), vp.data_ptr(),
+                                  static_cast<const int32_t*>(table.data_ptr()), static_cast<const int32_t*>(ptr(cu)),
+                                  static_cast<const int32_t*>(lens.data_ptr()), qs, ks, vs, ptr(qw), ptr(kw),
+                                  static_cast<const float*>(ptr(rope)), T, p.B, Hq, p.Hkv, p.num_blocks, p.block_size,
+                                  p.max_blocks, p.d, t.rot, t.max_pos, t.eps, inter, code, t.weight, on.stream());
+        }),
         "fa_append_paged");
   written(kp);
   written(vp);
@@ -393,17 +414,20 @@ PyObject* extend_paged(PyObject* const* a, Py_ssize_t n) {
   check_out(q, o);
   On on(q);
   on.with(kp).with(vp).with(table).with(lens).with(cu).with(ws).with(o).with(l);
-  const Tensor out = out_like(q, o);
-  const Tensor lse = l ? *l : at::empty({T, Hq}, at::TensorOptions(q.device()).dtype(at::kFloat));
-  if (!ws) {
-    const size_t need = abi.extend_paged_workspace_size(T, Hq, p.Hkv, p.d);
-    ws = bytes(q, need < 256 ? 256 : need);
-  }
-  check(abi.extend_paged(q.data_ptr(), kp.data_ptr(), vp.data_ptr(), static_cast<const int32_t*>(table.data_ptr()),
-                         static_cast<const int32_t*>(ptr(cu)), static_cast<const int32_t*>(lens.data_ptr()), out.data_ptr(),
-                         static_cast<float*>(lse.data_ptr()), qs, T, p.B, Hq, p.Hkv, p.num_blocks, p.block_size,
-                         p.max_blocks, p.d, scale, causal, static_cast<int>(window), code, ws->data_ptr(), ws->nbytes(),
-                         on.stream()),
+  Opt out, lse;
+  check(without_gil([&] {
+          out = out_like(q, o);
+          lse = l ? *l : at::empty({T, Hq}, at::TensorOptions(q.device()).dtype(at::kFloat));
+          if (!ws) {
+            const size_t need = abi.extend_paged_workspace_size(T, Hq, p.Hkv, p.d);
+            ws = bytes(q, need < 256 ? 256 : need);
+          }
+          return abi.extend_paged(q.data_ptr(), kp.data_ptr(), vp.data_ptr(), static_cast<const int32_t*>(table.data_ptr()),
+                                  static_cast<const int32_t*>(ptr(cu)), static_cast<const int32_t*>(lens.data_ptr()),
+                                  ptr(out), static_cast<float*>(ptr(lse)), qs, T, p.B, Hq, p.Hkv, p.num_blocks, p.block_size,
+                                  p.max_blocks, p.d, scale, causal, static_cast<int>(window), code, ptr(ws), ws->nbytes(),
+                                  on.stream());
+        }),
         "fa_extend_paged");
   written(o);
   written(l);
