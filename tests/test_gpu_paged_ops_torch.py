@@ -1,5 +1,7 @@
 """The norm-and-rotate, append and chunk attention calls among torch's other operations and Python's
-other threads: versions of tensors written in place, calls that wait for the device."""
+other threads: versions of tensors written in place, frozen inputs of the differentiable form, calls
+that wait for the device."""
+import itertools
 import threading
 import time
 
@@ -59,6 +61,37 @@ def test_inference_tensors_have_no_version():
         assert torch.equal(fa.extend_paged(q, kp, vp, table, lens, cu, out=torch.empty_like(q))[0],
                            fa.extend_paged(q, kp, vp, table, lens, cu)[0])
     assert fa.device_status() == fa.FA_OK
+
+
+def allocations(f):
+    """(f's result, how many blocks of device memory it asked for)."""
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    r = f()
+    return r, torch.cuda.memory_stats()["allocation.all.allocated"] - before
+
+
+@pytest.mark.parametrize("trains", [t for t in itertools.product([False, True], repeat=4) if any(t)])
+def test_frozen_inputs_cost_nothing(trains):
+    """Gradients of the inputs that train are norm_rope_backward's; a frozen side is not computed, a
+    frozen weight's gradient not summed."""
+    gen = torch.Generator().manual_seed(42)
+    q, gq = (torch.randn(2, 4, 30, 64, generator=gen).to(BF16).cuda() for _ in range(2))
+    k, gk = (torch.randn(2, 2, 30, 64, generator=gen).to(BF16).cuda() for _ in range(2))
+    qw, kw = (1 + 0.3 * torch.randn(64, generator=gen).to(BF16).cuda() for _ in range(2))
+    rope = rope_table(30, 64).cuda()
+    want = fa.norm_rope_backward(q, k, gq, gk, qw, kw, rope)
+    ins = [t.clone().requires_grad_(r) for t, r in zip((q, k, qw, kw), trains)]
+    y = fa.qk_norm_rope(*ins, rope=rope)
+    leaves = [t for t in ins if t.requires_grad]
+    got, blocks = allocations(lambda: torch.autograd.grad(y, leaves, (gq, gk)))
+    for g, w in zip(got, [w for w, r in zip(want, trains) if r]):
+        if g.dim() == 4:
+            assert torch.equal(g, w)
+        else:  # one side alone is summed in another order: the rounding to bf16 may be the next one
+            assert ((g.float() - w.float()).abs() <= torch.finfo(BF16).eps * w.float().abs()).all()
+    sides = [s for s in (0, 1) if trains[s] or trains[2 + s]]
+    sums = trains[2] + trains[3]
+    assert blocks == len(sides) + sums + (sums > 0)  # rows' gradients, weights', the sums' workspace
 
 
 @pytest.mark.parametrize("which", ["norm_rope", "norm_rope_backward", "append_paged", "extend_paged"])

@@ -539,7 +539,7 @@ def norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope=
     float32 in a fixed order and come in the weights' dtype.
     """
     return (_COMPILED or _compiled()).norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, eps,
-                                                         interleaved, workspace)
+                                                         interleaved, workspace, True, True)
 
 
 class _QKNormRope(torch.autograd.Function):
@@ -555,9 +555,20 @@ class _QKNormRope(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, gq, gk=None):
         q, k, q_weight, k_weight, rope, positions = ctx.saved_tensors
-        dq, dk, dqw, dkw = norm_rope_backward(q, k, _readable(gq), None if gk is None else _readable(gk), q_weight,
-                                              k_weight, rope, positions, *ctx.how)
-        return dq, dk, dqw, dkw, None, None, None, None
+        eps, interleaved = ctx.how
+        # A frozen side (neither its rows nor its weight want a gradient) is left out, a frozen
+        # weight's sum too.
+        need = ctx.needs_input_grad
+        sides = [s for s, x in enumerate((q, k)) if x is not None and (need[s] or need[2 + s])]
+        x, g, w, want = ([v[s] for s in sides] + [None] for v in ((q, k), (gq, gk), (q_weight, k_weight), need[2:4]))
+        two = len(sides) == 2
+        got = (_COMPILED or _compiled()).norm_rope_backward(
+            x[0], x[1], _readable(g[0]), _readable(g[1]) if two else None, w[0], w[1], rope, positions, eps, interleaved,
+            None, want[0], bool(want[1]))
+        grads = [None] * 8
+        for i, s in enumerate(sides):
+            grads[s], grads[2 + s] = got[i], got[2 + i]
+        return tuple(grads)
 
 
 def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6,

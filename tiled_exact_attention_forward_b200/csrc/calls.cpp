@@ -259,9 +259,10 @@ PyObject* norm_rope(PyObject* const* a, Py_ssize_t n) {
   return k ? tuple({q_out, k_out}) : wrap(q_out);
 }
 
-// q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, eps, interleaved, workspace
+// q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, eps, interleaved, workspace; whether
+// q_weight's and k_weight's gradients are wanted
 PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
-  arguments(n, 11);
+  arguments(n, 13);
   const Tensor q = first_tensor(a[0], "q"), gq = tensor(a[2], "dq_out");
   const Opt k = optional(a[1], "k"), gk = optional(a[3], "dk_out"), qw = optional(a[4], "q_weight"),
             kw = optional(a[5], "k_weight"), rope = optional(a[6], "rope"), pos = optional(a[7], "positions");
@@ -276,6 +277,7 @@ PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
   const Turn t = turn_of(q.scalar_type(), qw, kw, rope, a[8], r.d);
   const long long ps = position_stride(pos, r);
   const int inter = truth(a[9]);
+  const bool want_qw = qw && truth(a[11]), want_kw = kw && truth(a[12]);
   const fa_dtype code = dtype_code(q.scalar_type());
   int64_t st[18] = {};
   strides_of(q, r.packed, st);
@@ -299,10 +301,10 @@ PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
             dk = grad_like(*k);
             strides_of(*dk, r.packed, st + 15);
           }
-          if (qw) dqw = new_like(*qw);
-          if (kw) dkw = new_like(*kw);
+          if (want_qw) dqw = new_like(*qw);
+          if (want_kw) dkw = new_like(*kw);
           size_t ws_bytes = 0;
-          if (qw || kw) {
+          if (want_qw || want_kw) {
             if (!ws) ws = bytes(q, abi.norm_rope_backward_workspace_size(r.d));
             ws_bytes = ws->nbytes();
           }
