@@ -94,6 +94,57 @@ def test_frozen_inputs_cost_nothing(trains):
     assert blocks == len(sides) + sums + (sums > 0)  # rows' gradients, weights', the sums' workspace
 
 
+@pytest.mark.parametrize("layout", ["projection", "slice", "expanded"])
+@pytest.mark.parametrize("frozen", [None, 0, 1])
+def test_rotation_alone_does_not_keep_its_rows(layout, frozen):
+    """Without the norm the inputs can be freed before the backward, whose gradients are laid out as if
+    they were there."""
+    gen = torch.Generator().manual_seed(43)
+    rope = rope_table(400, 64).cuda()
+
+    def rows(H):
+        if layout == "projection":
+            return torch.randn(2, 400, H, 64, generator=gen).cuda(), lambda t: t.transpose(1, 2)
+        if layout == "slice":
+            return torch.randn(2, 400, 3 * H, 64, generator=gen).cuda(), lambda t: t[:, :, H:2 * H].transpose(1, 2)
+        return torch.randn(2, 1, 400, 64, generator=gen).cuda(), lambda t: t.expand(2, H, 400, 64)
+
+    leaves, xs, want = [], [], []
+    grads = [torch.randn(2, H, 400, 64, generator=gen).cuda() for H in (4, 2)]
+    for s, H in enumerate((4, 2)):
+        t, view = rows(H)
+        leaves.append(t.requires_grad_(s != frozen))
+        xs.append(view(t * 2.0))
+        x = view(t.detach())
+        dx = fa.norm_rope_backward(x, None, grads[s], None, rope=rope, eps=None)[0]
+        assert torch.equal(dx, fa.norm_rope_backward(None, None, grads[s], None, rope=rope, eps=None)[0])
+        if layout != "expanded":
+            assert dx.stride() == torch.empty_like(x).stride()
+        again = t.detach().clone().requires_grad_()
+        want.append(torch.autograd.grad(view(again * 2.0), again, dx)[0])
+    y = fa.qk_norm_rope(*xs, rope=rope, eps=None)
+    before = torch.cuda.memory_allocated()
+    size = sum(t.numel() * 4 for t in leaves)
+    del xs
+    assert before - torch.cuda.memory_allocated() >= size
+    torch.autograd.backward(y, grads)
+    for s, t in enumerate(leaves):
+        assert t.grad is None if s == frozen else torch.allclose(t.grad, want[s], rtol=1e-6, atol=1e-6)
+
+
+def test_backward_of_the_rotation_alone_takes_rows_or_none():
+    g = torch.randn(1, 2, 8, 64, device="cuda")
+    rope = rope_table(8, 64).cuda()
+    with pytest.raises(TypeError, match="q must be a tensor"):
+        fa.norm_rope_backward(None, None, g, None, rope=rope)
+    with pytest.raises(TypeError, match="q must be a tensor"):
+        fa.norm_rope_backward(None, g, g, g, rope=rope, eps=None)
+    with pytest.raises(ValueError, match="go together"):
+        fa.norm_rope_backward(g, None, g, g, rope=rope, eps=None)
+    dq, dk, _, _ = fa.norm_rope_backward(None, None, g, g, rope=rope, eps=None)
+    assert torch.equal(dq, dk) and torch.equal(dq, fa.norm_rope_backward(g, None, g, None, rope=rope, eps=None)[0])
+
+
 @pytest.mark.parametrize("which", ["norm_rope", "norm_rope_backward", "append_paged", "extend_paged"])
 def test_other_threads_run_while_a_launch_waits(which):
     """The device is busy for about a second and its queue of launches fills up: a call then waits in the

@@ -533,21 +533,32 @@ def norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope=
     """Gradients of norm_rope: (dq, dk, dq_weight, dk_weight).
 
     q, k: the forward's inputs; dq_out, dk_out: the gradients of its outputs, of the
-    same sizes, rows contiguous.  k and dk_out may be None together (dk is then
-    None).  dq and dk are laid out as q and k are (dense in their strides' order).
+    same sizes, rows contiguous, other strides multiples of 16 bytes.  k and dk_out may
+    be None together (dk is then None).  With eps=None the rows are not read: q and k
+    may both be None.  dq and dk are laid out as q and k are (dense in their strides'
+    order), as the given gradients without them.
     A weight that is None has no gradient (None); weight gradients are summed in
     float32 in a fixed order and come in the weights' dtype.
     """
     return (_COMPILED or _compiled()).norm_rope_backward(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, eps,
-                                                         interleaved, workspace, True, True)
+                                                         interleaved, workspace, True, True, None, None)
+
+
+def _dense(rows, g):
+    """A new tensor for the gradient of rows of this (shape, strides): dense in their strides' order."""
+    t = torch.empty_like(torch.empty_strided(*rows, dtype=g.dtype, device="meta"), device=g.device)
+    return t if t.stride(-1) == 1 else torch.empty(rows[0], dtype=g.dtype, device=g.device)
 
 
 class _QKNormRope(torch.autograd.Function):
-    """Saves the inputs; the backward recomputes the rows' norms from them."""
+    """Saves the inputs; the backward recomputes the rows' norms from them.  The rotation alone
+    does not need them: then only their layouts are kept."""
 
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, rope, positions, eps, interleaved):
-        ctx.save_for_backward(q, k, q_weight, k_weight, rope, positions)
+        ctx.rows = [None if x is None else (x.shape, x.stride()) for x in (q, k)]
+        saved = (None, None) if eps is None else (q, k)
+        ctx.save_for_backward(*saved, q_weight, k_weight, rope, positions)
         ctx.how = (eps, interleaved)
         return norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved)
 
@@ -559,12 +570,14 @@ class _QKNormRope(torch.autograd.Function):
         # A frozen side (neither its rows nor its weight want a gradient) is left out, a frozen
         # weight's sum too.
         need = ctx.needs_input_grad
-        sides = [s for s, x in enumerate((q, k)) if x is not None and (need[s] or need[2 + s])]
-        x, g, w, want = ([v[s] for s in sides] + [None] for v in ((q, k), (gq, gk), (q_weight, k_weight), need[2:4]))
-        two = len(sides) == 2
-        got = (_COMPILED or _compiled()).norm_rope_backward(
-            x[0], x[1], _readable(g[0]), _readable(g[1]) if two else None, w[0], w[1], rope, positions, eps, interleaved,
-            None, want[0], bool(want[1]))
+        sides = [s for s in (0, 1) if ctx.rows[s] is not None and (need[s] or need[2 + s])]
+        g = [_readable((gq, gk)[s]) for s in sides]
+        out = [None if eps is not None else _dense(ctx.rows[s], t) for s, t in zip(sides, g)]
+        x, g, w, want, out = ([*v, None][:2] for v in ([(q, k)[s] for s in sides], g,
+                                                       [(q_weight, k_weight)[s] for s in sides],
+                                                       [need[2 + s] for s in sides], out))
+        got = (_COMPILED or _compiled()).norm_rope_backward(*x, *g, *w, rope, positions, eps, interleaved, None,
+                                                            want[0], bool(want[1]), *out)
         grads = [None] * 8
         for i, s in enumerate(sides):
             grads[s], grads[2 + s] = got[i], got[2 + i]

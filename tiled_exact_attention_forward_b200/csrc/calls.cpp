@@ -260,19 +260,24 @@ PyObject* norm_rope(PyObject* const* a, Py_ssize_t n) {
 }
 
 // q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, eps, interleaved, workspace; whether
-// q_weight's and k_weight's gradients are wanted
+// q_weight's and k_weight's gradients are wanted; outputs for dq and dk, or None
 PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
-  arguments(n, 13);
-  const Tensor q = first_tensor(a[0], "q"), gq = tensor(a[2], "dq_out");
-  const Opt k = optional(a[1], "k"), gk = optional(a[3], "dk_out"), qw = optional(a[4], "q_weight"),
-            kw = optional(a[5], "k_weight"), rope = optional(a[6], "rope"), pos = optional(a[7], "positions");
+  arguments(n, 15);
+  // The rotation alone needs no rows: sizes then come from the gradients.
+  const bool norm = a[8] != Py_None, rows = norm || a[0] != Py_None || a[1] != Py_None;
+  const Tensor q = first_tensor(a[rows ? 0 : 2], rows ? "q" : "dq_out"), gq = tensor(a[2], "dq_out");
+  const Opt k = optional(a[rows ? 1 : 3], "k"), gk = optional(a[3], "dk_out"), qw = optional(a[4], "q_weight"),
+            kw = optional(a[5], "k_weight"), rope = optional(a[6], "rope"), pos = optional(a[7], "positions"),
+            dqo = optional(a[13], "dq"), dko = optional(a[14], "dk");
   Opt ws = optional(a[10], "workspace");
   TORCH_CHECK_VALUE(k.has_value() == gk.has_value(), "k and dk_out go together");
-  TORCH_CHECK_VALUE(k || !kw, "k_weight needs k");
+  TORCH_CHECK_VALUE(k || (!kw && !dko), "k_weight and dk need k");
   const Rows r = rows_of(q, k);
   TORCH_CHECK_VALUE(gq.sizes() == q.sizes() && gq.scalar_type() == q.scalar_type(), "dq_out must have q's shape and dtype");
   TORCH_CHECK_VALUE(!k || (gk->sizes() == k->sizes() && gk->scalar_type() == k->scalar_type()),
                     "dk_out must have k's shape and dtype");
+  check_out(q, dqo);
+  if (k) check_out(*k, dko);
   check_workspace(ws);
   const Turn t = turn_of(q.scalar_type(), qw, kw, rope, a[8], r.d);
   const long long ps = position_stride(pos, r);
@@ -287,7 +292,7 @@ PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
     strides_of(*gk, r.packed, st + 9);
   }
   On on(q);
-  on.with(k).with(gq).with(gk).with(qw).with(kw).with(rope).with(pos).with(ws);
+  on.with(k).with(gq).with(gk).with(qw).with(kw).with(rope).with(pos).with(ws).with(dqo).with(dko);
   // Laid out as x where x is dense, contiguous where not (expanded views).
   auto grad_like = [](const Tensor& x) {
     Tensor g = at::empty_like(x, x.options().requires_grad(false));
@@ -295,10 +300,10 @@ PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
   };
   Opt dq, dk, dqw, dkw;
   check(without_gil([&] {
-          dq = grad_like(q);
+          dq = dqo ? *dqo : grad_like(q);
           strides_of(*dq, r.packed, st + 12);
           if (k) {
-            dk = grad_like(*k);
+            dk = dko ? *dko : grad_like(*k);
             strides_of(*dk, r.packed, st + 15);
           }
           if (want_qw) dqw = new_like(*qw);
@@ -308,12 +313,14 @@ PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
             if (!ws) ws = bytes(q, abi.norm_rope_backward_workspace_size(r.d));
             ws_bytes = ws->nbytes();
           }
-          return abi.norm_rope_backward(q.data_ptr(), ptr(k), gq.data_ptr(), ptr(gk), ptr(dq), ptr(dk), st, ptr(qw), ptr(kw),
-                                        ptr(dqw), ptr(dkw), static_cast<const float*>(ptr(rope)),
+          return abi.norm_rope_backward(norm ? q.data_ptr() : nullptr, norm ? ptr(k) : nullptr, gq.data_ptr(), ptr(gk),
+                                        ptr(dq), ptr(dk), st, ptr(qw), ptr(kw), ptr(dqw), ptr(dkw), static_cast<const float*>(ptr(rope)),
                                         static_cast<const int32_t*>(ptr(pos)), ps, r.B, r.Hq, r.Hk, r.N, r.d, t.rot,
                                         t.max_pos, t.eps, inter, code, t.weight, ptr(ws), ws_bytes, on.stream());
         }),
         "fa_norm_rope_backward");
+  written(dqo);
+  written(dko);
   return tuple({dq, dk, dqw, dkw});
 }
 
