@@ -146,7 +146,7 @@ struct Run {
 // Everything else sits in static shared memory, whose addresses are constants: pointers
 // to it cost no registers.
 struct Ctl {
-  uint32_t bad[4][BN / 32];          // keys of a tile whose block lies outside the pool
+  alignas(16) uint32_t bad[4][BN / 32];  // keys of a tile whose block lies outside the pool (read as uint4)
   Piece piece[NP];
   // Barriers, by the arrivals that they count: one, a warpgroup's, the piece readers'.
   uint64_t q_full[2], q_empty[2];
@@ -165,6 +165,7 @@ struct Ctl {
   uint32_t tmem_base;
   int abort_flag;
 };
+static_assert(offsetof(Ctl, bad) % alignof(uint4) == 0 && alignof(Ctl) % alignof(uint4) == 0, "bad is read in 16-byte pieces");
 static_assert(kSmemBytes + sizeof(Ctl) + 64 <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ Seq seq_of(const ExtendArgs& a, int b) {

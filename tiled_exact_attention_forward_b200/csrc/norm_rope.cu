@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(THREADS)
   }
 
   if (NORM && a.partials != nullptr) {
-    __shared__ float sm[P][D];
+    __shared__ alignas(16) float sm[P][D];  // written in 16-byte pieces
     const Lane e = lane_of<F32, D, INTER>(s, a.rot);
     char* row = reinterpret_cast<char*>(sm[threadIdx.x / L]);
     store4<F32>(row + e.lo, pack<F32>(dw[0], dw[1]));
