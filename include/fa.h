@@ -402,8 +402,11 @@ FA_API size_t fa_extend_paged_workspace_size(int T, int Hq, int Hkv, int d);
  *                 aligned, contents ignored on entry.  Calls that may run at the
  *                 same time need workspaces of their own.
  * A block id outside [0, num_blocks) is skipped and recorded as in fa_decode_paged.
- * A non-finite value row that a token sees makes its own output non-finite; it may
- * do so, as 0 * inf, to the outputs of the tokens of the same chunk that precede it.
+ * A non-finite value row makes the outputs of the tokens that see it non-finite.  As
+ * 0 * inf it may do so to tokens that do not see it, that come before it or whose window
+ * has moved past it: those of the same group of 2 * floor(128 / G) new tokens, counted
+ * from the sequence's first new one, under the same key head, where one of the group sees
+ * it.  Their lse and all other outputs do not change.
  */
 FA_API fa_status fa_extend_paged(const void* q, const void* kpool, const void* vpool,
                                  const int32_t* block_table, const int32_t* cu_tokens,

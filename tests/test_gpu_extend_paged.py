@@ -212,6 +212,41 @@ def test_masked_keys_may_be_non_finite():
     assert torch.equal(o[:128], want[:128]) and o[129].isnan().all()
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("causal,window,row", [
+    (True, 100, 150),    # behind the window of the later tokens of the first group
+    (True, 100, 290),    # before and behind tokens of the third
+    (True, 0, 399),      # the last token's own
+    (False, 100, 150),
+    (True, 30, 169),     # behind every window: of the chunk's own group, no token sees it
+])
+def test_reach_of_a_non_finite_value_row(value, causal, window, row):
+    """Tokens that see the row come out non-finite; others may within its group of 64 tokens and its key
+    head; every other output, and every lse, keeps its bits."""
+    m, n, G = 200, 400, 4                       # positions 200 .. 399; groups of 2 * 128 / G = 64 tokens
+    q, kp, vp, table, cu, lens = make([m, 30], [n, 300], 2 * G, 2, 16, BF16, seed=34)
+    run = lambda v: fa.extend_paged(q.cuda(), kp.cuda(), v.cuda(), table.cuda(), lens.cuda(), cu_tokens=cu.cuda(),  # noqa: E731
+                                    causal=causal, window=window)
+    want, wl = run(vp)
+    v2 = vp.clone()
+    v2[table[0, row // 16], 1, row % 16] = value  # sequence 0, key head 1: query heads 4 .. 7
+    o, lse = run(v2)
+    assert fa.device_status() == fa.FA_OK
+    place = torch.arange(n - m, n)
+    sees = torch.ones(m, dtype=torch.bool)
+    if causal:
+        sees &= row <= place
+    if window:
+        sees &= row > place - window
+    assert not o[:m, G:][sees.cuda()].isfinite().any()
+    group = torch.arange(m) // 64
+    near = torch.isin(group, group[sees])       # groups with a token that sees the row
+    assert torch.equal(lse, wl)
+    assert torch.equal(o[:, :G], want[:, :G]) and torch.equal(o[m:], want[m:])
+    assert torch.equal(o[:m][~near.cuda()], want[:m][~near.cuda()])
+    assert sees.any() == (window != 30)
+
+
 def test_lowest_and_large_scores():
     """Queries scaled until one key takes all the weight, and scores far below zero."""
     q, kp, vp, table, cu, lens = make([5], [300], 4, 2, 16, BF16, seed=19)

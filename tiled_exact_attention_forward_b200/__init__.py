@@ -633,7 +633,8 @@ def extend_paged(q, kpool, vpool, block_table, seqlens, cu_tokens=None, causal: 
     Returns (o [T, Hq, d], lse [T, Hq] float32); o = 0 and lse = -inf for a token that
     sees no key; tokens outside every sequence keep what out and lse held.  Calls that
     may overlap need workspaces of their own (the default makes one).  An out-of-range
-    block id of a used block is skipped and reported by device_status().
+    block id of a used block is skipped and reported by device_status().  A non-finite value
+    row that a token sees may reach others of the chunk (include/fa.h says which).
     """
     return (_COMPILED or _compiled()).extend_paged(q, kpool, vpool, block_table, seqlens, cu_tokens, causal, window,
                                                    _scale_arg(scale), workspace, out, lse)
