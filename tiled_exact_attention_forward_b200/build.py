@@ -135,11 +135,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError(f"nvcc link failed with exit code {r.returncode}")
+    # The C library does not need the module, which a machine without Python's or torch's headers
+    # cannot build.
+    os.replace(tmp, LIB_PATH)
     calls_tmp, r = calls.result()
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError(f"the host compiler failed on calls.cpp with exit code {r.returncode}")
-    os.replace(tmp, LIB_PATH)
+        raise RuntimeError(f"the host compiler failed on calls.cpp with exit code {r.returncode}; {LIB_NAME} is built")
     os.replace(calls_tmp, CALLS_PATH)
     return LIB_PATH
 
