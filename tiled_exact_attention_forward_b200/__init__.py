@@ -479,12 +479,16 @@ def _compiled():
     global _COMPILED
     if _COMPILED is None:
         lib = _lib()
+        from .build import built_for
+
         try:
             from . import _calls
+            if _calls.built_for != built_for():
+                raise ImportError(f"built for {_calls.built_for}, this is {built_for()}")
         except ImportError as e:
             raise ImportError(
-                f"_calls.so is missing or was built for another Python or torch ({e}): build it with "
-                "`python -m tiled_exact_attention_forward_b200.build`"
+                f"the extension module _calls is missing or was built for another Python or torch ({e}): build it "
+                "with `python -m tiled_exact_attention_forward_b200.build`"
             ) from e
         entries = (lib.fa_norm_rope, lib.fa_norm_rope_backward, lib.fa_norm_rope_backward_workspace_size,
                    lib.fa_append_paged, lib.fa_extend_paged, lib.fa_extend_paged_workspace_size)

@@ -16,7 +16,9 @@ IEEE-rounded ones; every other kernel calls its fast instructions explicitly and
 fast-math flags it was measured with.
 
 csrc/calls.cpp, the compiled side of some of the Python calls, becomes the extension
-module _calls.so beside it (host code only, against torch's headers).
+module _calls beside it (host code only, against torch's headers).  It serves the Python
+and the torch that it was built for alone: its file name carries Python's tag, and it is
+built again when built_for() is no longer what the last build noted.
 """
 from __future__ import annotations
 
@@ -35,7 +37,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libfa_b200.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 CALLS_SOURCE = os.path.join(CSRC, "calls.cpp")
-CALLS_PATH = os.path.join(HERE, "_calls.so")
+CALLS_PATH = os.path.join(HERE, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON_FLAGS = [
@@ -66,18 +68,37 @@ def flags_for(src: str):
     return [*ARCH_FLAGS, *COMMON_FLAGS, *([] if name in EXACT_MATH_SOURCES else FAST_MATH)]
 
 
-def _inputs():
-    files = [CALLS_SOURCE] + sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-    files += glob.glob(os.path.join(ROOT, "include", "*.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+def _fresh(path, files) -> bool:
+    """`path` is there and no older than this script, the C header or any of `files`."""
+    files = [*files, *glob.glob(os.path.join(ROOT, "include", "*.h")), os.path.abspath(__file__)]
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in files)
+
+
+def library_up_to_date() -> bool:
+    headers = [f for pattern in ("*.cuh", "*.h") for f in glob.glob(os.path.join(CSRC, pattern))]
+    return _fresh(LIB_PATH, sources() + headers)
+
+
+def built_for() -> str:
+    """The Python, torch and C++ ABI that the extension module is compiled against."""
+    import torch
+
+    return f"{sys.implementation.cache_tag} torch-{torch.__version__} abi-{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+
+
+def _stamp() -> str:
+    return os.path.join(OBJ_DIR, "calls.stamp")
+
+
+def calls_up_to_date() -> bool:
+    if not (_fresh(CALLS_PATH, [CALLS_SOURCE]) and os.path.exists(_stamp())):
+        return False
+    with open(_stamp()) as f:
+        return f.read() == built_for()
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(CALLS_PATH)):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return library_up_to_date() and calls_up_to_date()
 
 
 def _compile(src: str, extra, verbose: bool):
@@ -92,12 +113,14 @@ def _compile(src: str, extra, verbose: bool):
 def calls_command(out: str):
     """The host compiler's command for the extension module: the one torch was built to go with (a
     compiler that links a C++ runtime of its own would not share its exceptions)."""
+    import torch
     from torch.utils import cpp_extension
 
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     libs = ["torch_python", "torch", "torch_cpu", "torch_cuda", "c10", "c10_cuda"]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DFA_BUILT_FOR="{built_for()}"',
             *(f"-I{d}" for d in inc), "-o", out, CALLS_SOURCE,
             *(f"-L{d}" for d in cpp_extension.library_paths()), *(f"-l{n}" for n in libs)]
 
@@ -107,17 +130,20 @@ def _build_calls(verbose: bool):
     cmd = calls_command(tmp)
     if verbose:
         print(" ".join(cmd), flush=True)
-    return tmp, subprocess.run(cmd, cwd=CSRC, capture_output=True, text=True)
+    r = subprocess.run(cmd, cwd=CSRC, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"the host compiler failed on calls.cpp with exit code {r.returncode} ({LIB_NAME} is built)")
+    if os.path.exists(_stamp()):
+        os.remove(_stamp())
+    os.replace(tmp, CALLS_PATH)
+    with open(_stamp(), "w") as f:
+        f.write(built_for())
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    """Compile every kernel for sm_100a into libfa_b200.so; returns its path."""
-    if not force and up_to_date():
-        return LIB_PATH
-    os.makedirs(OBJ_DIR, exist_ok=True)
+def _build_library(verbose: bool, extra_flags):
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 1)) as ex:
-        calls = ex.submit(_build_calls, verbose)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 1)) as ex:
         results = list(ex.map(lambda s: _compile(s, extra_flags, verbose), srcs))
     objs = []
     for (obj, r), src in zip(results, srcs):
@@ -135,14 +161,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError(f"nvcc link failed with exit code {r.returncode}")
-    # The C library does not need the module, which a machine without Python's or torch's headers
-    # cannot build.
     os.replace(tmp, LIB_PATH)
-    calls_tmp, r = calls.result()
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError(f"the host compiler failed on calls.cpp with exit code {r.returncode}; {LIB_NAME} is built")
-    os.replace(calls_tmp, CALLS_PATH)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
+    """Compile every kernel for sm_100a into libfa_b200.so, and the extension module; returns the
+    library's path.  What is up to date stays as it is."""
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    # Side by side; the library does not need the module, which a machine without Python's or
+    # torch's headers cannot build.
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        calls = ex.submit(_build_calls, verbose) if force or not calls_up_to_date() else None
+        if force or not library_up_to_date():
+            _build_library(verbose, extra_flags)
+    if calls is not None:
+        calls.result()
     return LIB_PATH
 
 

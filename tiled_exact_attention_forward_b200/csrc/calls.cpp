@@ -486,4 +486,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__calls() {
+  PyObject* m = PyModule_Create(&module);
+  // The Python and torch that this file was compiled against, for __init__.py to compare.
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", FA_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}
