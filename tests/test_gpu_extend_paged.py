@@ -340,6 +340,24 @@ def test_pool_offsets_past_32_bits():
     assert_within(lse, l_ref, lb, "lse")
 
 
+def test_query_offsets_past_32_bits():
+    """Queries and outputs of more than 2^31 elements: 8193 sequences of 64 new tokens over shared blocks."""
+    B, m, Hq, Hkv, block = 8193, 64, 32, 4, 16
+    kp, vp, table, _, _ = paged_cache([1], [128], Hkv, block, BF16, seed=35)
+    table = table.expand(B, 8).contiguous()
+    lens = (m + torch.arange(B) * 7 % 65).int()
+    cu = (torch.arange(B + 1) * m).int()
+    q = torch.empty(B * m, Hq, 128, dtype=BF16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(36))
+    assert q.numel() > 1 << 31
+    o, lse = fa.extend_paged(q, kp.cuda(), vp.cuda(), table.cuda(), lens.cuda(), cu_tokens=cu.cuda())
+    assert fa.device_status() == fa.FA_OK
+    for b in (0, 4096, B - 1):
+        part = slice(b * m, (b + 1) * m)
+        o_ref, l_ref, ob, lb = attend(q[part].cpu(), kp, vp, table[:1], torch.tensor([0, m]), lens[b:b + 1])
+        assert_within(o[part], o_ref, ob, f"o of sequence {b}")
+        assert_within(lse[part], l_ref, lb, f"lse of sequence {b}")
+
+
 def test_tokens_outside_every_sequence_and_shared_blocks():
     """cu_tokens that begins past 0, sequences that share their first blocks, the same block twice."""
     q, kp, vp, table, cu, lens = make([4, 6, 70], [100, 120, 200], 4, 2, 16, BF16, seed=28, extra=9)

@@ -300,3 +300,24 @@ def test_captured_and_replayed():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, run()))
+
+
+def test_row_offsets_past_32_bits():
+    """Queries, outputs and gradients of more than 2^31 elements: the last rows are read and written at
+    their places."""
+    T, Hq = (1 << 31) // (32 * 128) + 70, 32
+    x = torch.empty(T, Hq + 1, 128, dtype=BF16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(22))
+    q, k = x[:, :Hq], x[:, Hq:]
+    assert q.numel() > 1 << 31
+    pos = (torch.arange(T, device="cuda") % 100).int()
+    rope = rope_table(100, 128).cuda()
+    yq, yk = fa.norm_rope(q, k, rope=rope, positions=pos)
+    gq, gk, _, _ = fa.norm_rope_backward(q, k, yq, yk, rope=rope, positions=pos)
+    assert fa.device_status() == fa.FA_OK
+    for part in (slice(0, 70), slice(T - 70, T)):
+        want = fa.norm_rope(q[part], k[part], rope=rope, positions=pos[part])
+        assert torch.equal(yq[part], want[0]) and torch.equal(yk[part], want[1])
+        g = fa.norm_rope_backward(q[part], k[part], yq[part], yk[part], rope=rope, positions=pos[part])
+        assert torch.equal(gq[part], g[0]) and torch.equal(gk[part], g[1])
+    z, b = norm_rotate(q[-3:].cpu(), None, rope.cpu()[pos[-3:].cpu().long()][:, None], 1e-6, False)
+    assert_within(yq[-3:], z, b, "last rows")
