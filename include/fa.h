@@ -351,7 +351,7 @@ FA_API fa_status fa_norm_rope_backward(const void* q, const void* k, const void*
  *                 Token t of sequence b takes position
  *                 seqlens[b] - cu_tokens[b + 1] + t.
  *   q, q_out    : [T][Hq][d], q at q_stride, q_out contiguous (q_out may be q where
- *                 that is contiguous); both NULL: no queries.
+ *                 that is contiguous); both NULL: no queries, q_weight is not read.
  *   q_weight, k_weight, rope, rot, max_pos, eps, interleaved, weight_dtype: as
  *                 fa_norm_rope (without norm and rotation the keys are copied).
  * Two new tokens must not share a place (sequences may share blocks of earlier
@@ -377,7 +377,10 @@ FA_API size_t fa_extend_paged_workspace_size(int T, int Hq, int Hkv, int d);
  * Chunk attention: packed new tokens attend to their sequences' paged caches, which
  * hold them already (fa_append_paged).  Hq = G * Hkv query heads, query head h
  * reading key head h / G.  With one token a sequence this is fa_decode_paged's
- * attention with grouped heads.
+ * attention with grouped heads, with one rounding more: the weights enter the product
+ * with V in the 16-bit type, as in fa_forward (relative error up to 2^-8 in bf16, 2^-11
+ * in fp16, of each term; lse and the sum of the weights are float32), where
+ * fa_decode_paged keeps them in float32.
  *
  *   q           : [T][Hq][d] (dtype FA_BF16 or FA_FP16, d = 128), heads contiguous,
  *                 tokens q_stride elements apart (a multiple of 16 bytes,
@@ -450,7 +453,11 @@ FA_API fa_status fa_selftest_exp2_poly(const float* x, float* y, long long n, vo
 /* Static, human-readable name of a status code. */
 FA_API const char* fa_status_string(fa_status status);
 
-/* Library ABI version (major * 100 + minor). */
+/* Library ABI version (major * 100 + minor).  It rises when an entry point that was
+ * there before takes or does something else (1.04: float32 partials in fa_merge).  An
+ * entry point added since is known by its symbol: fa_norm_rope, fa_append_paged and
+ * fa_extend_paged came with 1.04 unchanged, so a program that may meet an older library
+ * looks them up (dlsym) or is refused by the linker. */
 FA_API int fa_version(void);
 
 #ifdef __cplusplus

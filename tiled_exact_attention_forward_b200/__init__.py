@@ -633,7 +633,9 @@ def extend_paged(q, kpool, vpool, block_table, seqlens, cu_tokens=None, causal: 
     pools, block_table, seqlens and cu_tokens as append_paged takes them, Hq a
     multiple of the pools' heads (query head h reads key head h * Hkv // Hq).  Token i
     of the m new ones of a sequence of length n sits at position n - m + i and sees
-    the keys up to itself (causal), the last `window` of them with window > 0.
+    the keys up to itself (causal), the last `window` of them with window > 0 (2^29 at most).
+    Weights enter the product with v in the 16-bit type, as in forward (decode_paged keeps
+    them in float32).
     Returns (o [T, Hq, d], lse [T, Hq] float32); o = 0 and lse = -inf for a token that
     sees no key; tokens outside every sequence keep what out and lse held.  Calls that
     may overlap need workspaces of their own (the default makes one).  An out-of-range

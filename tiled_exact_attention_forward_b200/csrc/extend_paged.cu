@@ -31,17 +31,22 @@
 // without a key are not issued, other such rows are zeroed in shared memory before
 // the MMA, since their weights are zero but 0 * NaN is not.
 //
-// What bounds it, and what it measured (device time):
+// What bounds it, and what it measured (a run of calls, or a replayed graph of them, which take
+// the same time; at 1965 MHz, the first 0.1 s or so, before the card's power limit of 1000 W lowers
+// the clock; in brackets after a second of such calls, with the clock that was left):
 //   2048 tokens of a prompt at 14336 .. 16383, 32 heads over 8: the tensor cores through
-//     the S -> softmax -> PV chain of a two-tile item, as in fwd_tc.cu; 425 us, 1210 TFLOP/s;
-//   64 single tokens, 512 .. 8192 keys, 32 heads over 8: the cache's bytes; 196 us, 5.8 TB/s
-//     (88 % of the copy rate); an item's edges (Q, first S, last PV, epilogue) cost as much
-//     as one or two key tiles, of the 118 a CTA takes here;
-//   24 x 5 tokens, 100 .. 4000 keys, 16 heads over 16: 90 us, 5.3 TB/s (80 %), shorter items;
-//   512 single tokens over 600 keys: 316 us, 4.0 TB/s (61 %): five key tiles an item, the
-//     edges' chains no longer hidden by the next item's loads (two stages a ring);
-//   17 ragged pieces under a window of 1024: 95 us, 515 TFLOP/s: a third of the key
-//     tiles are partly masked, and a CTA has 27 in three or four items to level out;
+//     the S -> softmax -> PV chain of a two-tile item, as in fwd_tc.cu; 429 us, 1200 TFLOP/s
+//     (508 us, 1014 TFLOP/s at 1620 MHz);
+//   64 single tokens, 512 .. 8192 keys, 32 heads over 8: the cache's bytes; 195 us, 5.8 TB/s
+//     (88 % of the copy rate; 230 us at 1515 MHz); an item's edges (Q, first S, last PV,
+//     epilogue) cost as much as one or two key tiles, of the 118 a CTA takes here;
+//   24 x 5 tokens, 100 .. 4000 keys, 16 heads over 16: 90 us, 5.3 TB/s (80 %), shorter items
+//     (102 us at 1605 MHz);
+//   512 single tokens over 600 keys: 316 us, 4.0 TB/s (61 %; 338 us at 1845 MHz): five key tiles
+//     an item, the edges' chains no longer hidden by the next item's loads (two stages a ring);
+//   17 ragged pieces under a window of 1024: 95 us, 515 TFLOP/s (102 us at 1830 MHz): a third of
+//     the key tiles are partly masked, and a CTA has 27 in three or four items to level out;
+//   8192 tokens of a fresh prompt, 32 heads over 8: 475 us, 1157 TFLOP/s (562 us at 1640 MHz);
 //   one token over 512 keys: 14.2 us: launch, planning, a key tile's latency, the join.
 // The kernel's text is kept near 90 KB with single issue sites and loops that are not
 // unrolled: at 225 KB the sixteen warps' roles displaced one another in the instruction cache.
@@ -1245,8 +1250,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             f2_unpack(x2, x0, x1);
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             acc[(e >> 1) & 3] = f2_add(acc[(e >> 1) & 3], f2_pack(p0, p1));
-            // P in 16 bits, the MMA's type: relative error 2^-9 (bf16) a weight, below the
-            // output's own rounding after the sum; l adds the unrounded values.
+            // P in 16 bits, the MMA's type: relative error up to 2^-8 (bf16; fp16 2^-11) a weight,
+            // the size of the output's own rounding, less where many keys share the weight; l adds
+            // the unrounded values.  Measured against 64 bits (bf16, relative norm): 0.0021 to 0.0023,
+            // the output's rounding alone 0.0017.
             pk[e >> 1] = pack2<T>(p0, p1);
           }
           asm volatile(
