@@ -94,6 +94,17 @@ def test_frozen_inputs_cost_nothing(trains):
     assert blocks == len(sides) + sums + (sums > 0)  # rows' gradients, weights', the sums' workspace
 
 
+@pytest.mark.parametrize("eps", [1e-6, None])
+@pytest.mark.parametrize("with_k", [False, True])
+def test_a_table_that_wants_a_gradient_gets_none(eps, with_k):
+    """Frozen rows under a rotation table that is a parameter: the backward runs and leaves it without one."""
+    q = torch.randn(1, 2, 8, 64, device="cuda")
+    rope = rope_table(8, 64).cuda().requires_grad_()
+    y = fa.qk_norm_rope(q, q if with_k else None, rope=rope, eps=eps)
+    sum(t.sum() for t in (y if with_k else (y,))).backward()
+    assert rope.grad is None
+
+
 @pytest.mark.parametrize("layout", ["projection", "slice", "expanded"])
 @pytest.mark.parametrize("frozen", [None, 0, 1])
 def test_rotation_alone_does_not_keep_its_rows(layout, frozen):

@@ -575,6 +575,9 @@ class _QKNormRope(torch.autograd.Function):
         # weight's sum too.
         need = ctx.needs_input_grad
         sides = [s for s in (0, 1) if ctx.rows[s] is not None and (need[s] or need[2 + s])]
+        grads = [None] * 8
+        if not sides:  # only the table wants one, and it has none
+            return tuple(grads)
         g = [_readable((gq, gk)[s]) for s in sides]
         out = [None if eps is not None else _dense(ctx.rows[s], t) for s, t in zip(sides, g)]
         x, g, w, want, out = ([*v, None][:2] for v in ([(q, k)[s] for s in sides], g,
@@ -582,7 +585,6 @@ class _QKNormRope(torch.autograd.Function):
                                                        [need[2 + s] for s in sides], out))
         got = (_COMPILED or _compiled()).norm_rope_backward(*x, *g, *w, rope, positions, eps, interleaved, None,
                                                             want[0], bool(want[1]), *out)
-        grads = [None] * 8
         for i, s in enumerate(sides):
             grads[s], grads[2 + s] = got[i], got[2 + i]
         return tuple(grads)
