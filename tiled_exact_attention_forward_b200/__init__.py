@@ -548,46 +548,41 @@ def norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope=
                                                          interleaved, workspace, True, True, None, None)
 
 
-def _dense(rows, g):
-    """A new tensor for the gradient of rows of this (shape, strides): dense in their strides' order."""
-    t = torch.empty_like(torch.empty_strided(*rows, dtype=g.dtype, device="meta"), device=g.device)
-    return t if t.stride(-1) == 1 else torch.empty(rows[0], dtype=g.dtype, device=g.device)
-
-
 class _QKNormRope(torch.autograd.Function):
     """Saves the inputs; the backward recomputes the rows' norms from them.  The rotation alone
-    does not need them: then only their layouts are kept."""
+    does not need them: then only their strides are kept, for the gradients' layout."""
 
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, rope, positions, eps, interleaved):
-        ctx.rows = [None if x is None else (x.shape, x.stride()) for x in (q, k)]
-        saved = (None, None) if eps is None else (q, k)
-        ctx.save_for_backward(*saved, q_weight, k_weight, rope, positions)
-        ctx.how = (eps, interleaved)
+        if eps is None:
+            ctx.save_for_backward(None, None, q_weight, k_weight, rope, positions)
+            ctx.how = (eps, interleaved, q.stride(), None if k is None else k.stride())
+        else:
+            ctx.save_for_backward(q, k, q_weight, k_weight, rope, positions)
+            ctx.how = (eps, interleaved, None, None)
         return norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, gq, gk=None):
         q, k, q_weight, k_weight, rope, positions = ctx.saved_tensors
-        eps, interleaved = ctx.how
+        eps, interleaved, q_strides, k_strides = ctx.how
         # A frozen side (neither its rows nor its weight want a gradient) is left out, a frozen
         # weight's sum too.
-        need = ctx.needs_input_grad
-        sides = [s for s in (0, 1) if ctx.rows[s] is not None and (need[s] or need[2 + s])]
-        grads = [None] * 8
-        if not sides:  # only the table wants one, and it has none
-            return tuple(grads)
-        g = [_readable((gq, gk)[s]) for s in sides]
-        out = [None if eps is not None else _dense(ctx.rows[s], t) for s, t in zip(sides, g)]
-        x, g, w, want, out = ([*v, None][:2] for v in ([(q, k)[s] for s in sides], g,
-                                                       [(q_weight, k_weight)[s] for s in sides],
-                                                       [need[2 + s] for s in sides], out))
-        got = (_COMPILED or _compiled()).norm_rope_backward(*x, *g, *w, rope, positions, eps, interleaved, None,
-                                                            want[0], bool(want[1]), *out)
-        for i, s in enumerate(sides):
-            grads[s], grads[2 + s] = got[i], got[2 + i]
-        return tuple(grads)
+        need_q, need_k, need_qw, need_kw = ctx.needs_input_grad[:4]
+        q_side, k_side = need_q or need_qw, gk is not None and (need_k or need_kw)
+        dq = dk = dqw = dkw = None
+        run = (_COMPILED or _compiled()).norm_rope_backward
+        if q_side and k_side:
+            dq, dk, dqw, dkw = run(q, k, _readable(gq), _readable(gk), q_weight, k_weight, rope, positions, eps,
+                                   interleaved, None, need_qw, need_kw, q_strides, k_strides)
+        elif q_side:
+            dq, _, dqw, _ = run(q, None, _readable(gq), None, q_weight, None, rope, positions, eps, interleaved, None,
+                                need_qw, False, q_strides, None)
+        elif k_side:
+            dk, _, dkw, _ = run(k, None, _readable(gk), None, k_weight, None, rope, positions, eps, interleaved, None,
+                                need_kw, False, k_strides, None)
+        return dq, dk, dqw, dkw, None, None, None, None
 
 
 def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6,

@@ -7,12 +7,14 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/ExpandUtils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
+#include <vector>
 
 #include "../../include/fa.h"
 
@@ -57,6 +59,17 @@ double number(PyObject* o) {
 int truth(PyObject* o) {
   const int v = PyObject_IsTrue(o);
   if (v < 0) throw Failed{};
+  return v;
+}
+// n integers of a tuple.
+std::optional<std::vector<int64_t>> integers(PyObject* o, int64_t n) {
+  if (o == Py_None) return std::nullopt;
+  TORCH_CHECK_TYPE(PyTuple_Check(o) && PyTuple_GET_SIZE(o) == n, "strides must be a tuple of ", n, " integers");
+  std::vector<int64_t> v;
+  for (int64_t i = 0; i < n; ++i) {
+    v.push_back(PyLong_AsLongLong(PyTuple_GET_ITEM(o, i)));
+    if (v.back() == -1 && PyErr_Occurred()) throw Failed{};
+  }
   return v;
 }
 void* ptr(const Opt& t) { return t ? t->data_ptr() : nullptr; }
@@ -260,24 +273,22 @@ PyObject* norm_rope(PyObject* const* a, Py_ssize_t n) {
 }
 
 // q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, eps, interleaved, workspace; whether
-// q_weight's and k_weight's gradients are wanted; outputs for dq and dk, or None
+// q_weight's and k_weight's gradients are wanted; q's and k's strides, where they are None themselves
+// but dq and dk are to be laid out as they were, or None
 PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
   arguments(n, 15);
   // The rotation alone needs no rows: sizes then come from the gradients.
   const bool norm = a[8] != Py_None, rows = norm || a[0] != Py_None || a[1] != Py_None;
   const Tensor q = first_tensor(a[rows ? 0 : 2], rows ? "q" : "dq_out"), gq = tensor(a[2], "dq_out");
   const Opt k = optional(a[rows ? 1 : 3], "k"), gk = optional(a[3], "dk_out"), qw = optional(a[4], "q_weight"),
-            kw = optional(a[5], "k_weight"), rope = optional(a[6], "rope"), pos = optional(a[7], "positions"),
-            dqo = optional(a[13], "dq"), dko = optional(a[14], "dk");
+            kw = optional(a[5], "k_weight"), rope = optional(a[6], "rope"), pos = optional(a[7], "positions");
   Opt ws = optional(a[10], "workspace");
   TORCH_CHECK_VALUE(k.has_value() == gk.has_value(), "k and dk_out go together");
-  TORCH_CHECK_VALUE(k || (!kw && !dko), "k_weight and dk need k");
+  TORCH_CHECK_VALUE(k || !kw, "k_weight needs k");
   const Rows r = rows_of(q, k);
   TORCH_CHECK_VALUE(gq.sizes() == q.sizes() && gq.scalar_type() == q.scalar_type(), "dq_out must have q's shape and dtype");
   TORCH_CHECK_VALUE(!k || (gk->sizes() == k->sizes() && gk->scalar_type() == k->scalar_type()),
                     "dk_out must have k's shape and dtype");
-  check_out(q, dqo);
-  if (k) check_out(*k, dko);
   check_workspace(ws);
   const Turn t = turn_of(q.scalar_type(), qw, kw, rope, a[8], r.d);
   const long long ps = position_stride(pos, r);
@@ -292,18 +303,20 @@ PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
     strides_of(*gk, r.packed, st + 9);
   }
   On on(q);
-  on.with(k).with(gq).with(gk).with(qw).with(kw).with(rope).with(pos).with(ws).with(dqo).with(dko);
-  // Laid out as x where x is dense, contiguous where not (expanded views).
-  auto grad_like = [](const Tensor& x) {
-    Tensor g = at::empty_like(x, x.options().requires_grad(false));
-    return g.stride(-1) == 1 ? g : new_like(x);
+  on.with(k).with(gq).with(gk).with(qw).with(kw).with(rope).with(pos).with(ws);
+  // Laid out as x, dense in its strides' order; contiguous where that would part a row's elements
+  // (expanded views).
+  auto grad_like = [](const Tensor& x, const std::optional<std::vector<int64_t>>& strides) {
+    const auto dense = at::infer_dense_strides(x.sizes(), strides ? at::IntArrayRef(*strides) : x.strides());
+    return dense.back() == 1 ? at::empty_strided(x.sizes(), dense, x.options().requires_grad(false)) : new_like(x);
   };
+  const auto q_strides = integers(a[13], q.dim()), k_strides = integers(a[14], q.dim());
   Opt dq, dk, dqw, dkw;
   check(without_gil([&] {
-          dq = dqo ? *dqo : grad_like(q);
+          dq = grad_like(q, q_strides);
           strides_of(*dq, r.packed, st + 12);
           if (k) {
-            dk = dko ? *dko : grad_like(*k);
+            dk = grad_like(*k, k_strides);
             strides_of(*dk, r.packed, st + 15);
           }
           if (want_qw) dqw = new_like(*qw);
@@ -319,8 +332,6 @@ PyObject* norm_rope_backward(PyObject* const* a, Py_ssize_t n) {
                                         t.max_pos, t.eps, inter, code, t.weight, ptr(ws), ws_bytes, on.stream());
         }),
         "fa_norm_rope_backward");
-  written(dqo);
-  written(dko);
   return tuple({dq, dk, dqw, dkw});
 }
 
