@@ -1,5 +1,5 @@
 """The norm-and-rotate, append and chunk attention calls among torch's other operations and Python's
-other threads: versions of tensors written in place, frozen inputs of the differentiable form, calls
+other threads: given outputs, versions of tensors written in place, frozen inputs of the differentiable form, calls
 that wait for the device."""
 import itertools
 import threading
@@ -22,6 +22,44 @@ def small_cache():
     kp, vp, table, cu, lens = paged_cache([2, 5], [20, 33], 2, 16, BF16, seed=40, pad=0.0)
     x = torch.randn(7, 8, 128, generator=torch.Generator().manual_seed(41)).to(BF16).cuda()
     return x[:, :4].clone(), x[:, 4:6].clone(), x[:, 6:].clone(), *(t.cuda() for t in (kp, vp, table, lens, cu))
+
+
+def test_given_outputs_at_their_strides():
+    """Outputs into parts of larger tensors, in another order of dimensions, and onto the inputs where a
+    fused projection left them: the same bits, and nothing beside them is touched."""
+    gen = torch.Generator().manual_seed(44)
+    x = torch.randn(2, 30, 10, 128, generator=gen).to(BF16).cuda()   # [B, N, Hq + Hk + 2, d]
+    rope, w = rope_table(30, 64).cuda(), 1 + 0.3 * torch.randn(128, generator=gen).to(BF16).cuda()
+    q, k = x[:, :, 1:6].transpose(1, 2), x[:, :, 6:8].transpose(1, 2)
+    want = fa.norm_rope(q, k, w, None, rope)
+    wide = torch.full((2, 30, 10, 128), 7.0, dtype=BF16, device="cuda")
+    got = fa.norm_rope(q, k, w, None, rope, q_out=wide[:, :, 1:6].transpose(1, 2), k_out=wide[:, :, 6:8].transpose(1, 2))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert (wide[:, :, 0] == 7.0).all() and (wide[:, :, 8:] == 7.0).all()
+    before = x.clone()
+    got = fa.norm_rope(q, k, w, None, rope, q_out=q, k_out=k)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(x[:, :, 0], before[:, :, 0]) and torch.equal(x[:, :, 8:], before[:, :, 8:])
+
+
+def test_queries_turned_where_they_lie_and_pools_inside_larger_ones():
+    q, k, v, kp, vp, table, lens, cu = small_cache()
+    rope = rope_table(40, 128).cuda()
+    big = [torch.cat([p[:1], p, p[:1]]) for p in (kp, vp)]
+    edges = [(p[0].clone(), p[-1].clone()) for p in big]
+    want = fa.append_paged(k, v, kp, vp, table, lens, cu, rope, q)
+    o, lse = fa.extend_paged(want, kp, vp, table, lens, cu)
+    fa.append_paged(k, v, big[0][1:-1], big[1][1:-1], table, lens, cu, rope, q, q_out=q)
+    assert torch.equal(q, want)
+    for p, small, (a, b) in zip(big, (kp, vp), edges):
+        assert torch.equal(p[1:-1], small) and torch.equal(p[0], a) and torch.equal(p[-1], b)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        got = fa.extend_paged(q, big[0][1:-1], big[1][1:-1], table, lens, cu)
+    torch.cuda.current_stream().wait_stream(stream)
+    assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+    assert fa.device_status() == fa.FA_OK
 
 
 def test_an_overwritten_tensor_is_missed_by_the_backward_that_saved_it():
